@@ -8,6 +8,7 @@
 
 #include "aqlm.h"
 #include "aqlm_internal.h"
+#include "mx4_internal.h"
 
 namespace {
 
@@ -135,6 +136,9 @@ aqlm_status check_workspace(const void* ws, size_t ws_bytes, size_t need, const 
 }  // namespace
 
 namespace aqlm {
+uint32_t* status_word() { return device_status_ptr(); }
+int status_of(cudaError_t e) { return from_cuda(e); }
+
 uint64_t current_context_id() {
   using GetCurrentFn = CUresult (*)(CUcontext*);
   using GetIdFn = CUresult (*)(CUcontext, unsigned long long*);

@@ -1,0 +1,99 @@
+// Device-side pieces shared by the mx4 kernels: where a block's scale lies, scale and
+// e2m1 decoding, and conversions of the 16-bit types.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "aqlm_device.cuh"
+#include "mx4_internal.h"
+
+namespace aqlm {
+
+// Byte of block c of row r in tiled scales with `tiles` 512-byte tiles along K.
+__device__ __forceinline__ size_t mx4_scale_at(int r, int c, int tiles) {
+  return (static_cast<size_t>(r >> 7) * tiles + (c >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (c & 3);
+}
+
+// The fp32 value of a scale byte (exact; NaN codes give NaN).
+template <int FORMAT>
+__device__ __forceinline__ float mx4_scale_value(uint32_t b) {
+  if constexpr (FORMAT == kMxfp4) {
+    // 2^(b - 127): the exponent field; code 0 is the subnormal 2^-127
+    const uint32_t bits = b == 255 ? 0x7FFFFFFFu : max(b << 23, 0x00400000u);
+    return __uint_as_float(bits);
+  } else {
+    uint32_t h2;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h2) : "r"(b));
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xFFFF)));
+  }
+}
+
+// Eight e2m1 codes (low four bits first) as four fp16 pairs, in order.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+
+__device__ __forceinline__ float2 b2_to_f2(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint32_t f2_to_b2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A pair of 16-bit values of `TYPE` (kF16, kBf16) to and from fp32.
+template <int TYPE>
+__device__ __forceinline__ float2 pair_to_f2(uint32_t v) {
+  return TYPE == kF16 ? h2_to_f2(v) : b2_to_f2(v);
+}
+template <int TYPE>
+__device__ __forceinline__ uint32_t f2_to_pair(float lo, float hi) {
+  return TYPE == kF16 ? f2_to_h2_rn(lo, hi) : f2_to_b2_rn(lo, hi);
+}
+
+// One value at index i of an array of `TYPE`.
+template <int TYPE>
+__device__ __forceinline__ float load_value(const void* p, size_t i) {
+  if constexpr (TYPE == kF16) return __half2float(static_cast<const __half*>(p)[i]);
+  else if constexpr (TYPE == kBf16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  else return static_cast<const float*>(p)[i];
+}
+template <int TYPE>
+__device__ __forceinline__ void store_value(void* p, size_t i, float v) {
+  if constexpr (TYPE == kF16) static_cast<__half*>(p)[i] = __float2half_rn(v);
+  else if constexpr (TYPE == kBf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<float*>(p)[i] = v;
+}
+
+// Launch with programmatic stream serialisation: the kernel's start overlaps the end of
+// the one before it, and its grid_dependency_wait() orders its memory accesses after it.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                                     cudaStream_t stream, int cluster, Args... args) {
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+}  // namespace aqlm

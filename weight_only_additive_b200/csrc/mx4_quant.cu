@@ -1,0 +1,333 @@
+// Quantisation to and dequantisation from microscaled 4-bit floating point.
+//
+// Both are one pass bound by HBM: a thread takes 16 (quantise) or 32 (dequantise)
+// consecutive values of a row.
+#include "mx4_device.cuh"
+
+namespace aqlm {
+namespace {
+
+constexpr int kThreads = 256;
+// Grid-stride beyond this many CTAs.
+constexpr long long kMaxBlocks = 148LL * 64;
+
+// idx / units, in 32 bits where the total allows it.
+__device__ __forceinline__ long long row_of(long long idx, int units, bool small) {
+  return small ? static_cast<long long>(static_cast<uint32_t>(idx) / static_cast<uint32_t>(units)) : idx / units;
+}
+
+// 32 bytes at p (16-byte aligned; `wide`: 32-byte aligned).
+__device__ __forceinline__ void load32(const void* p, bool wide, uint32_t (&v)[8]) {
+  uint4 a, b;
+  if (wide) {
+    ldg_nc_v8(p, a, b);
+  } else {
+    a = ldg_nc_v4(p);
+    b = ldg_nc_v4(static_cast<const uint8_t*>(p) + 16);
+  }
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+__device__ __forceinline__ void store32(void* p, bool wide, const uint32_t (&v)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+  } else {
+    uint4* q = static_cast<uint4*>(p);
+    q[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    q[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// Two bytes of e2m1 pairs: (a0, a1) in the low byte, (a2, a3) in the next, and so on.
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&a)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(a[0]), "f"(a[1]), "f"(a[2]), "f"(a[3]), "f"(a[4]), "f"(a[5]), "f"(a[6]), "f"(a[7]));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t to_e4m3(float v) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(r) : "f"(v));
+  return r & 0xFF;
+}
+
+// The e2m1 code of x / unit from exact products in 64 bits (a midpoint has 3 bits, the
+// unit at most 28): one more for every midpoint below |x|, ties to the even code.
+__device__ __noinline__ uint32_t exact_e2m1(float x, double unit) {
+  const double a = fabs(static_cast<double>(x));
+  uint32_t code = 0;
+#pragma unroll
+  for (int i = 0; i < 7; ++i) {
+    const double mid = i < 4 ? 0.25 + 0.5 * i : i < 6 ? i - 1.5 : 5.0;
+    const double border = mid * unit;
+    code += a > border || (a == border && (i & 1)) ? 1u : 0u;
+  }
+  return code | (__float_as_uint(x) >> 31 << 3);
+}
+
+// e4m3 of the exact quotient amax / (6 gamma), inv = 1 / (6 gamma) to 64 bits.  The
+// 64-bit product is within 2^-51 of the quotient; a quotient that is not a tie stays
+// 2^-33 away from every tie (its terms have 24 and 27 bits), so what lies within 2^-40
+// of an fp32 value is that value, and anything else goes to the odd fp32 neighbour: the
+// conversion then rounds it as it would the quotient.
+__device__ __forceinline__ uint32_t scale_e4m3(float amax, double inv) {
+  const double v = fmin(static_cast<double>(amax) * inv, 1024.0);
+  const float f = __double2float_rn(v);
+  const double r = v - static_cast<double>(f);
+  uint32_t bits = __float_as_uint(f);
+  if (fabs(r) > v * 0x1p-40) {
+    if (r < 0) --bits;
+    bits |= 1u;
+  }
+  return to_e4m3(__uint_as_float(bits));
+}
+
+// A thread's 16 values and the largest of their magnitudes.
+template <int TYPE>
+struct Values {
+  uint32_t raw[TYPE == kF32 ? 16 : 8];
+
+  __device__ __forceinline__ void load(const void* x, size_t at, bool wide) {
+    uint32_t(*half)[8] = reinterpret_cast<uint32_t(*)[8]>(raw);
+    const uint8_t* p = static_cast<const uint8_t*>(x) + at * (TYPE == kF32 ? 4 : 2);
+    load32(p, wide, half[0]);
+    if constexpr (TYPE == kF32) load32(p + 32, wide, half[1]);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (uint32_t& r : raw) r = 0;
+  }
+  // magnitudes compare as whole numbers; infinities and NaN come out on top
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    if constexpr (TYPE == kF32) {
+      uint32_t m = 0;
+#pragma unroll
+      for (uint32_t r : raw) m = max(m, r & 0x7FFFFFFFu);
+      return m;
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (uint32_t r : raw) m = __vmaxu2(m, r & 0x7FFF7FFFu);
+      return max(m & 0xFFFFu, m >> 16);
+    }
+  }
+  static __device__ __forceinline__ float as_float(uint32_t bits) {
+    if constexpr (TYPE == kF32) return __uint_as_float(bits);
+    else return pair_to_f2<TYPE>(bits).x;
+  }
+  __device__ __forceinline__ void eight(int h, float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (TYPE == kF32) {
+        f[i] = __uint_as_float(raw[8 * h + i]);
+      } else {
+        const float2 p = pair_to_f2<TYPE>(raw[4 * h + i / 2]);
+        f[i] = i & 1 ? p.y : p.x;
+      }
+    }
+  }
+};
+
+// Rows of `units` 16-value pieces, the last ones past K filling the row's last scale tile.
+template <int FORMAT, int TYPE>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const void* __restrict__ x, uint8_t* __restrict__ packed,
+                                                            uint8_t* __restrict__ scales,
+                                                            const float* __restrict__ tensor_scale, long long total,
+                                                            int units, int K, int tiles, bool small, bool wide) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const float gamma = FORMAT == kNvfp4 && tensor_scale ? *tensor_scale : 1.0f;
+  const bool gamma_bad = !(gamma >= 0.0f && gamma <= 3.402823466e38f);
+  const double inv6 = gamma > 0.0f ? 1.0 / (6.0 * static_cast<double>(gamma)) : 0.0;
+  const int lane = threadIdx.x & 31;
+  const long long stride = static_cast<long long>(gridDim.x) * kThreads;
+  for (long long base = static_cast<long long>(blockIdx.x) * kThreads + (threadIdx.x & ~31); base < total;
+       base += stride) {
+    const long long idx = base + lane;
+    const long long row = row_of(idx < total ? idx : 0, units, small);
+    const int u = static_cast<int>(idx - row * units);
+    const bool inside = idx < total && u * 16 < K;
+    Values<TYPE> v;
+    if (inside) v.load(x, static_cast<size_t>(row) * K + static_cast<size_t>(u) * 16, wide);
+    else v.zero();
+    uint32_t top = v.amax_bits();
+    if (FORMAT == kMxfp4) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    const bool bad = top >= (TYPE == kF32 ? 0x7F800000u : TYPE == kBf16 ? 0x7F80u : 0x7C00u);
+    const float amax = bad ? 0.0f : Values<TYPE>::as_float(top);
+
+    uint32_t code;    // the block's scale
+    uint2 q = {0, 0};  // 16 e2m1 codes
+    float f[8];
+    if constexpr (FORMAT == kMxfp4) {
+      const uint32_t e = __float_as_uint(amax) >> 23;
+      code = e > 2 ? e - 2 : 0;
+      const float inv = __uint_as_float((254u - code) << 23);  // 2^(127 - code), exact
+      if (!bad) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          v.eight(h, f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] *= inv;
+          (h ? q.y : q.x) = to_e2m1x8(f);
+        }
+      } else {
+        code = 0xFF;
+      }
+    } else {
+      code = scale_e4m3(amax, inv6);
+      if (bad || gamma_bad) {
+        code = 0x7F;
+      } else if (code != 0) {
+        // fp32 quotients are within 2^-21; where that much to either side gives two
+        // codes, the exact comparison decides
+        const float s = mx4_scale_value<kNvfp4>(code);
+        const float unit = s * gamma;
+        const bool plain = unit > 0x1p-100f && unit < 0x1p100f;
+        const float inv = plain ? __fdividef(1.0f, unit) : 0.0f;
+        const float below = inv * (1.0f - 0x1p-20f), above = inv * (1.0f + 0x1p-20f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float g[8];
+          v.eight(h, f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) g[i] = f[i] * above;
+          const uint32_t hi = to_e2m1x8(g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) g[i] = f[i] * below;
+          uint32_t lo = to_e2m1x8(g);
+          const uint32_t differ = plain ? hi ^ lo : 0xFFFFFFFFu;
+          if (differ) {
+            const double exact_unit = static_cast<double>(s) * static_cast<double>(gamma);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (differ >> (4 * i) & 0xF)
+                lo = (lo & ~(0xFu << (4 * i))) | exact_e2m1(f[i], exact_unit) << (4 * i);
+          }
+          (h ? q.y : q.x) = lo;
+        }
+      }
+    }
+    if (inside) *reinterpret_cast<uint2*>(packed + (static_cast<size_t>(row) * K + static_cast<size_t>(u) * 16) / 2) = q;
+
+    // the four scales of a tile's row together
+    if (!inside) code = 0;
+    constexpr int kPer = FORMAT == kMxfp4 ? 2 : 1;  // threads per block
+    uint32_t four = code << (8 * ((lane / kPer) & 3));
+    four |= __shfl_xor_sync(0xFFFFFFFFu, four, kPer);
+    four |= __shfl_xor_sync(0xFFFFFFFFu, four, 2 * kPer);
+    if (idx < total && (lane & (4 * kPer - 1)) == 0)
+      *reinterpret_cast<uint32_t*>(scales + mx4_scale_at(static_cast<int>(row), u / kPer, tiles)) = four;
+  }
+}
+
+// Rows of K / 32 pieces of 32 values.
+template <int FORMAT, int TYPE>
+__global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* __restrict__ packed,
+                                                              const uint8_t* __restrict__ scales,
+                                                              const float* __restrict__ tensor_scale,
+                                                              void* __restrict__ out, long long total, int units,
+                                                              int tiles, bool small, bool wide) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const float gamma = tensor_scale ? *tensor_scale : 1.0f;
+  const long long stride = static_cast<long long>(gridDim.x) * kThreads;
+  for (long long idx = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; idx < total; idx += stride) {
+    const long long row = row_of(idx, units, small);
+    const int u = static_cast<int>(idx - row * units);
+    const uint4 w = ldg_nc_v4(packed + static_cast<size_t>(idx) * 16);
+    float s[2];
+    if constexpr (FORMAT == kMxfp4) {
+      s[0] = s[1] = mx4_scale_value<FORMAT>(scales[mx4_scale_at(static_cast<int>(row), u, tiles)]);
+    } else {
+      const uint32_t two = *reinterpret_cast<const uint16_t*>(scales + mx4_scale_at(static_cast<int>(row), 2 * u, tiles));
+      s[0] = mx4_scale_value<FORMAT>(two & 0xFF);
+      s[1] = mx4_scale_value<FORMAT>(two >> 8);
+    }
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    uint8_t* o = static_cast<uint8_t*>(out) + static_cast<size_t>(idx) * 32 * (TYPE == kF32 ? 4 : 2);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v[TYPE == kF32 ? 16 : 8];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t pairs[4];
+        e2m1x8_to_f16(words[2 * h + j], pairs);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 q = h2_to_f2(pairs[i]);
+          const float lo = __fmul_rn(__fmul_rn(q.x, s[h]), gamma), hi = __fmul_rn(__fmul_rn(q.y, s[h]), gamma);
+          if constexpr (TYPE == kF32) {
+            v[8 * j + 2 * i] = __float_as_uint(lo);
+            v[8 * j + 2 * i + 1] = __float_as_uint(hi);
+          } else {
+            v[4 * j + i] = f2_to_pair<TYPE>(lo, hi);
+          }
+        }
+      }
+      uint32_t(*part)[8] = reinterpret_cast<uint32_t(*)[8]>(v);
+      if constexpr (TYPE == kF32) {
+        store32(o + 64 * h, wide, part[0]);
+        store32(o + 64 * h + 32, wide, part[1]);
+      } else {
+        store32(o + 32 * h, wide, part[0]);
+      }
+    }
+  }
+}
+
+unsigned blocks_for(long long total) {
+  const long long b = (total + kThreads - 1) / kThreads;
+  return static_cast<unsigned>(b < kMaxBlocks ? b : kMaxBlocks);
+}
+
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+
+template <int FORMAT, int TYPE>
+cudaError_t quantize_as(const void* x, uint8_t* packed, uint8_t* scales, const float* tensor_scale, int rows, int K,
+                        cudaStream_t stream) {
+  const int tiles = mx4_scale_tiles(K, FORMAT);
+  const int units = tiles * 4 * mx4_block(FORMAT) / 16;
+  const long long total = static_cast<long long>(rows) * units;
+  return launch_overlapped(quantize_kernel<FORMAT, TYPE>, blocks_for(total), kThreads, 0, stream, 1, x, packed, scales,
+                           tensor_scale, total, units, K, tiles, total <= 0xFFFFFFFFll, aligned32(x));
+}
+
+template <int FORMAT, int TYPE>
+cudaError_t dequantize_as(const Mx4& t, void* out, int K, cudaStream_t stream) {
+  const int units = K / 32;
+  const long long total = static_cast<long long>(t.rows) * units;
+  return launch_overlapped(dequantize_kernel<FORMAT, TYPE>, blocks_for(total), kThreads, 0, stream, 1, t.packed,
+                           t.scales, t.tensor_scale, out, total, units, mx4_scale_tiles(K, FORMAT),
+                           total <= 0xFFFFFFFFll, aligned32(out));
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_quantize(const void* x, int x_type, uint8_t* packed, uint8_t* scales,
+                                const float* tensor_scale, int rows, int K, int format, cudaStream_t stream) {
+#define MX4_CASE(f, t) \
+  if (format == f && x_type == t) return quantize_as<f, t>(x, packed, scales, tensor_scale, rows, K, stream);
+  MX4_CASE(kMxfp4, kF16) MX4_CASE(kMxfp4, kBf16) MX4_CASE(kMxfp4, kF32)
+  MX4_CASE(kNvfp4, kF16) MX4_CASE(kNvfp4, kBf16) MX4_CASE(kNvfp4, kF32)
+#undef MX4_CASE
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_mx4_dequantize(const Mx4& t, void* out, int out_type, int K, int format, cudaStream_t stream) {
+#define MX4_CASE(f, ty) \
+  if (format == f && out_type == ty) return dequantize_as<f, ty>(t, out, K, stream);
+  MX4_CASE(kMxfp4, kF16) MX4_CASE(kMxfp4, kBf16) MX4_CASE(kMxfp4, kF32)
+  MX4_CASE(kNvfp4, kF16) MX4_CASE(kNvfp4, kBf16) MX4_CASE(kNvfp4, kF32)
+#undef MX4_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace aqlm

@@ -23,6 +23,10 @@ EXPORTS = ("aqlm_matmul", "aqlm_matmul_path", "aqlm_dequantize", "aqlm_select_pa
            "aqlm_static_group_scratch_bytes", "aqlm_matmul_workspace_size", "aqlm_matmul_ws",
            "aqlm_input_grad_workspace_size", "aqlm_input_grad_ws")
 
+# Every exported symbol of include/mx4.h.
+MX4_EXPORTS = ("mx4_scales_bytes", "mx4_quantize", "mx4_dequantize", "mx4_matmul_workspace_size", "mx4_matmul",
+               "mx4_matmul_mx4", "mx4_input_grad_workspace_size", "mx4_input_grad")
+
 ABI_VERSION = 8
 
 # Site code aqlm_selftest_bounded_wait records in the device status word.
@@ -87,6 +91,7 @@ _lock = threading.Lock()
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_ll = ctypes.c_longlong
 
 
 def lib() -> ctypes.CDLL:
@@ -142,6 +147,24 @@ def lib() -> ctypes.CDLL:
                 L.aqlm_static_group_scratch_bytes.restype = ctypes.c_size_t
                 L.aqlm_selftest_bounded_wait.argtypes = [ctypes.c_uint, _vp]
                 L.aqlm_selftest_bounded_wait.restype = _i
+                L.mx4_scales_bytes.argtypes = [_ll, _ll, _i]
+                L.mx4_scales_bytes.restype = ctypes.c_size_t
+                L.mx4_quantize.argtypes = [_vp, _i, _vp, _vp, _vp, _ll, _ll, _i, _vp]
+                L.mx4_quantize.restype = _i
+                L.mx4_dequantize.argtypes = [_vp, _vp, _vp, _vp, _i, _ll, _ll, _i, _vp]
+                L.mx4_dequantize.restype = _i
+                L.mx4_matmul_workspace_size.argtypes = [_i, _ll, _ll, _ll, _i]
+                L.mx4_matmul_workspace_size.restype = ctypes.c_size_t
+                L.mx4_matmul.argtypes = [_vp, _i, _vp, _vp, _vp, _vp, _vp, _ll, _ll, _ll, _i, _vp, ctypes.c_size_t,
+                                         _vp]
+                L.mx4_matmul.restype = _i
+                L.mx4_matmul_mx4.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _ll, _ll, _ll, _i, _vp]
+                L.mx4_matmul_mx4.restype = _i
+                L.mx4_input_grad_workspace_size.argtypes = [_i, _ll, _ll, _ll, _i]
+                L.mx4_input_grad_workspace_size.restype = ctypes.c_size_t
+                L.mx4_input_grad.argtypes = [_vp, _i, _vp, _vp, _vp, _vp, _ll, _ll, _ll, _i, _vp, ctypes.c_size_t,
+                                             _vp]
+                L.mx4_input_grad.restype = _i
                 if L.aqlm_abi_version() != ABI_VERSION:
                     raise ImportError(f"libaqlm.so ABI {L.aqlm_abi_version()} != binding ABI {ABI_VERSION}")
                 _lib = L
@@ -259,3 +282,43 @@ def aqlm_matmul_group_host(problems, x_host, y_host, workspace, workspace_bytes,
 def aqlm_selftest_bounded_wait(timeout_us: int, stream=None):
     """Launch the bounded-wait self-test kernel (see include/aqlm.h)."""
     _check(lib().aqlm_selftest_bounded_wait(int(timeout_us), stream), "aqlm_selftest_bounded_wait")
+
+
+# microscaled 4-bit operators (include/mx4.h)
+def mx4_scales_bytes(rows, K, format) -> int:
+    return lib().mx4_scales_bytes(rows, K, format)
+
+
+def mx4_quantize(x, x_type, packed, scales, tensor_scale, rows, K, format, stream=None):
+    _check(lib().mx4_quantize(x, x_type, packed, scales, tensor_scale, rows, K, format, stream), "mx4_quantize")
+
+
+def mx4_dequantize(packed, scales, tensor_scale, out, out_type, rows, K, format, stream=None):
+    _check(lib().mx4_dequantize(packed, scales, tensor_scale, out, out_type, rows, K, format, stream),
+           "mx4_dequantize")
+
+
+def mx4_matmul_workspace_size(type, N, K, batch, format) -> int:
+    return lib().mx4_matmul_workspace_size(type, N, K, batch, format)
+
+
+def mx4_matmul(x, type, w_packed, w_scales, w_tensor_scale, bias, y, N, K, batch, format, workspace=None,
+               workspace_bytes=0, stream=None):
+    _check(lib().mx4_matmul(x, type, w_packed, w_scales, w_tensor_scale, bias, y, N, K, batch, format, workspace,
+                            workspace_bytes, stream), "mx4_matmul")
+
+
+def mx4_matmul_mx4(x_packed, x_scales, x_tensor_scale, w_packed, w_scales, w_tensor_scale, bias, y, y_type, N, K,
+                   batch, format, stream=None):
+    _check(lib().mx4_matmul_mx4(x_packed, x_scales, x_tensor_scale, w_packed, w_scales, w_tensor_scale, bias, y,
+                                y_type, N, K, batch, format, stream), "mx4_matmul_mx4")
+
+
+def mx4_input_grad_workspace_size(type, N, K, batch, format) -> int:
+    return lib().mx4_input_grad_workspace_size(type, N, K, batch, format)
+
+
+def mx4_input_grad(dy, type, w_packed, w_scales, w_tensor_scale, dx, N, K, batch, format, workspace=None,
+                   workspace_bytes=0, stream=None):
+    _check(lib().mx4_input_grad(dy, type, w_packed, w_scales, w_tensor_scale, dx, N, K, batch, format, workspace,
+                                workspace_bytes, stream), "mx4_input_grad")
