@@ -1,105 +1,428 @@
-// Products with a 4-bit weight matrix: 64 x 64 output tiles, both operands decoded to
-// fp32 in shared memory, 4 x 4 outputs a thread.
+// y = x . W^T + bias with both operands in microscaled 4 bits, on the block-scaled
+// tensor-core path (tcgen05.mma kind::mxf4 / kind::mxf4nvf4): the scales are applied
+// inside the MMA, sums are fp32.
+//
+// A CTA computes 128 tokens x NT features.  A stage is 256 values of K: 128-byte packed
+// rows of both operands by TMA (128-byte swizzle) and their scales as whole 512-byte
+// tiles, which tcgen05.cp spreads over the four TMEM lane quadrants as the MMA wants
+// them.  One thread loads, one issues copies and MMAs, eight warps write results.
+//
+// Work: one CTA per output tile, persistent over the SMs; where there are fewer tiles
+// than SMs a cluster of CTAs shares a tile along K and adds the fp32 partial tiles through
+// distributed shared memory, in rank order, so results do not depend on timing.
 #include "mx4_device.cuh"
 
 namespace aqlm {
 namespace {
 
-constexpr int kTile = 64, kStep = 32;
+constexpr int kRows = 128;           // tokens of a tile (MMA M)
+constexpr int kStageK = 256;         // values of K in a stage
+constexpr int kRowBytes = kStageK / 2;
+constexpr int kStepK = 64;           // values of K in one MMA
+constexpr int kThreads = 320;        // load warp, MMA warp, 8 epilogue warps
+constexpr int kEpilogue = 256;
+constexpr int kMaxSmem = 227 * 1024;
 
-// Value (r, k) of a 4-bit tensor, its tensor scale left out.
-template <int FORMAT>
-__device__ __forceinline__ float mx4_value(const Mx4& t, int r, int k, int K, int tiles) {
-  const uint32_t byte = t.packed[static_cast<size_t>(r) * (K / 2) + k / 2];
-  uint32_t h[4];
-  e2m1x8_to_f16(byte >> ((k & 1) * 4), h);
-  return h2_to_f2(h[0]).x * mx4_scale_value<FORMAT>(t.scales[mx4_scale_at(r, k / mx4_block(FORMAT), tiles)]);
+constexpr int round_pow2(int v) { return v <= 32 ? 32 : v <= 64 ? 64 : v <= 128 ? 128 : v <= 256 ? 256 : 512; }
+
+// Shapes that follow from the format and the tile width.
+template <int FORMAT, int NT>
+struct Plan {
+  static constexpr int kTilesK = kStageK / (4 * mx4_block(FORMAT));  // scale tiles of a stage along K
+  static constexpr int kTilesN = NT > 128 ? 2 : 1;                   // and along the features
+  static constexpr int kA = kRows * kRowBytes, kB = NT * kRowBytes;
+  static constexpr int kSa = kTilesK * 512, kSb = kTilesN * kTilesK * 512;
+  static constexpr int kStage = kA + kB + ((kSa + kSb + 1023) & ~1023);
+  static constexpr int kFit = (kMaxSmem - 2048) / kStage;
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  // TMEM columns: accumulators (two where they fit beside two stages' scales), then scales
+  static constexpr int kScaleCols = kTilesK * 4 * (1 + kTilesN);
+  static constexpr int kAccs = 2 * NT + 2 * kScaleCols <= 512 ? 2 : 1;
+  static constexpr int kFitScales = (512 - kAccs * NT) / kScaleCols;
+  static constexpr int kScaleBufs = kFitScales > kStages ? kStages : kFitScales;
+  static constexpr int kCols = round_pow2(kAccs * NT + kScaleBufs * kScaleCols);
+  static constexpr int kRedPitch = NT + 4;  // floats of a partial row: 16-byte stores of 8 lanes hit all banks
+  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStage + 2048;
+  static_assert(kStages >= 3 && kScaleBufs >= 2 && kCols <= 512, "");
+  static_assert(kRows * kRedPitch * 4 <= kStages * kStage, "");
+};
+
+struct ProductParams {
+  const uint8_t* xs;
+  const uint8_t* ws;
+  const float* gx;
+  const float* gw;
+  const void* bias;
+  void* y;
+  uint32_t* status;
+  int batch, N, K, tiles;  // tiles: scale tiles along K
+  int m_tiles, n_tiles, splits, y_type;
+};
+
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t smem) {
+  // 32 rows of 16 bytes, 8-row groups 128 bytes apart, no swizzle
+  const uint64_t desc = static_cast<uint64_t>((smem >> 4) & 0x3FFFu) | static_cast<uint64_t>(128u >> 4) << 32 |
+                        static_cast<uint64_t>(1u) << 46;
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// out[i][j] = sum_k a(i, k) b(j, k): a from 16-bit rows (A_TYPE) or a 4-bit tensor (-1),
-// b the weight (GRAD: its transpose).
-template <int FORMAT, int A_TYPE, int OUT_TYPE, bool GRAD>
-__global__ void __launch_bounds__(256) product_kernel(const void* a16, Mx4 a4, Mx4 w, const void* bias, void* out,
-                                                      int rows, int cols, int depth, int K) {
-  __shared__ float As[kStep][kTile + 1], Bs[kStep][kTile + 1];
+// Instruction descriptor of the block-scaled MMA: e2m1 operands (code 1), both K-major.
+//   bits 4-5 / 29-30 byte of the scale word that B's / A's scales start at
+//   bits 7-9 / 10-12 operand types, 17-22 N >> 3, 23 scale type (1: e8m0), 24-28 M >> 4
+template <int FORMAT>
+__host__ __device__ constexpr uint32_t mx4_idesc(uint32_t n, uint32_t sf) {
+  return sf << 4 | 1u << 7 | 1u << 10 | (n >> 3) << 17 | (FORMAT == kMxfp4 ? 1u : 0u) << 23 | (kRows >> 4) << 24 |
+         sf << 29;
+}
+
+template <int FORMAT>
+__device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                         uint32_t accumulate) {
+  if constexpr (FORMAT == kMxfp4) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate) : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate) : "memory");
+  }
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank) : "memory");
+  return v;
+}
+
+// bias[c .. c + 8) as fp32 (zeros without one; c + 8 <= N)
+__device__ __forceinline__ void bias8(const void* bias, int type, size_t c, float (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    b[i] = !bias ? 0.0f
+           : type == kF16  ? load_value<kF16>(bias, c + i)
+           : type == kBf16 ? load_value<kBf16>(bias, c + i)
+                           : load_value<kF32>(bias, c + i);
+}
+
+// v[0..8) * scale + bias to y[row][c ..); `vec`: rows of y are whole 16-byte units.
+__device__ __forceinline__ void put8(const ProductParams& p, int row, int c, const float* v, float scale, bool vec) {
+  const size_t at = static_cast<size_t>(row) * p.N + c;
+  if (vec && c + 8 <= p.N) {
+    float b[8], o[8];
+    bias8(p.bias, p.y_type, c, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = fmaf(v[i], scale, b[i]);
+    if (p.y_type == kF32) {
+      float4* q = reinterpret_cast<float4*>(static_cast<float*>(p.y) + at);
+      q[0] = make_float4(o[0], o[1], o[2], o[3]);
+      q[1] = make_float4(o[4], o[5], o[6], o[7]);
+    } else {
+      uint4 q;
+      if (p.y_type == kF16)
+        q = make_uint4(f2_to_h2_rn(o[0], o[1]), f2_to_h2_rn(o[2], o[3]), f2_to_h2_rn(o[4], o[5]), f2_to_h2_rn(o[6], o[7]));
+      else
+        q = make_uint4(f2_to_b2_rn(o[0], o[1]), f2_to_b2_rn(o[2], o[3]), f2_to_b2_rn(o[4], o[5]), f2_to_b2_rn(o[6], o[7]));
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + at) = q;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (c + i >= p.N) break;
+    if (p.y_type == kF32)
+      store_value<kF32>(p.y, at + i, fmaf(v[i], scale, p.bias ? load_value<kF32>(p.bias, c + i) : 0.0f));
+    else if (p.y_type == kF16)
+      store_value<kF16>(p.y, at + i, fmaf(v[i], scale, p.bias ? load_value<kF16>(p.bias, c + i) : 0.0f));
+    else
+      store_value<kBf16>(p.y, at + i, fmaf(v[i], scale, p.bias ? load_value<kBf16>(p.bias, c + i) : 0.0f));
+  }
+}
+
+template <int FORMAT, int NT>
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ CUtensorMap x_map,
+                                                              const __grid_constant__ CUtensorMap w_map,
+                                                              const ProductParams p) {
+  using P = Plan<FORMAT, NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[P::kStages], empty[P::kStages], acc_full[P::kAccs], acc_empty[P::kAccs];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t failed;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    failed = 0;
+    for (int i = 0; i < P::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < P::kAccs; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kEpilogue);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc(&tmem_slot, P::kCols);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  const uint32_t scale_tmem = tmem + P::kAccs * NT;
+
   grid_dependency_wait();
   grid_dependents_launch();
-  const int tiles = (K / mx4_block(FORMAT) + 3) / 4;
-  const int i0 = blockIdx.y * kTile, j0 = blockIdx.x * kTile, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < depth; k0 += kStep) {
-    for (int e = threadIdx.x; e < kTile * kStep; e += 256) {
-      const int i = e / kStep, k = e % kStep;
-      float v = 0.0f;
-      if (i0 + i < rows && k0 + k < depth) {
-        if constexpr (A_TYPE >= 0) v = load_value<A_TYPE>(a16, static_cast<size_t>(i0 + i) * depth + k0 + k);
-        else v = mx4_value<FORMAT>(a4, i0 + i, k0 + k, K, tiles);
+
+  const int k_stages = (p.K + kStageK - 1) / kStageK;
+  const int rank = p.splits > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int s0 = k_stages * rank / p.splits, s1 = k_stages * (rank + 1) / p.splits;
+  const int total = p.m_tiles * p.n_tiles;
+  const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
+  // a wait that gives up makes every later one in this CTA end at once
+  const auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+    if (failed) return false;
+    if (mbar_wait_bounded(bar, parity, p.status, site)) return true;
+    failed = 1;
+    return false;
+  };
+
+  if (warp == 0 && lane == 0) {
+    // ---- loads
+    const uint64_t keep = l2_policy_evict_last(), pass = l2_policy_evict_first();
+    const int x_row_tiles = (p.batch + 127) / 128, w_row_tiles = (p.N + 127) / 128;
+    uint32_t it = 0, landed = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step) {
+      const int m = t % p.m_tiles, n0 = (t / p.m_tiles) * NT;
+      for (int s = s0; s < s1 && ok; ++s, ++it) {
+        const int slot = it % P::kStages;
+        ok = wait(&empty[slot], ((it / P::kStages) & 1) ^ 1, kSitePipeEmpty);
+        if (!ok) break;
+        const uint32_t base = smem_addr(stages + slot * P::kStage);
+        const int c0 = s * P::kTilesK;
+        const uint32_t run = static_cast<uint32_t>(min(P::kTilesK, p.tiles - c0)) * 512;
+        const int wt = n0 / 128;
+        const int w_tiles = min(P::kTilesN, w_row_tiles - wt);
+        mbar_arrive_expect_tx(&full[slot], P::kA + P::kB + run * (1 + w_tiles));
+        tma_load_2d(base, &x_map, s * kRowBytes, m * kRows, &full[slot], keep);
+        tma_load_2d(base + P::kA, &w_map, s * kRowBytes, n0, &full[slot], p.m_tiles > 1 ? keep : pass);
+        const uint32_t sa = base + P::kA + P::kB, sb = sa + P::kSa;
+        bulk_load(sa, p.xs + (static_cast<size_t>(m) * p.tiles + c0) * 512, run, &full[slot]);
+        for (int j = 0; j < w_tiles; ++j)
+          bulk_load(sb + j * P::kSa, p.ws + (static_cast<size_t>(wt + j) * p.tiles + c0) * 512, run, &full[slot]);
+        landed = it + 1;
       }
-      As[k][i] = v;
     }
-    for (int e = threadIdx.x; e < kTile * kStep; e += 256) {
-      const int j = GRAD ? e % kTile : e / kStep, k = GRAD ? e / kTile : e % kStep;
-      float v = 0.0f;
-      if (j0 + j < cols && k0 + k < depth)
-        v = GRAD ? mx4_value<FORMAT>(w, k0 + k, j0 + j, K, tiles) : mx4_value<FORMAT>(w, j0 + j, k0 + k, K, tiles);
-      Bs[k][j] = v;
+    (void)x_row_tiles;
+    // copies still in flight after a failure land before the shared memory goes away
+    if (!ok)
+      for (uint32_t j = landed > P::kStages ? landed - P::kStages : 0; j < landed; ++j)
+        mbar_wait_bounded(&full[j % P::kStages], (j / P::kStages) & 1, p.status, kSitePipeFull);
+  } else if (warp == 1 && lane == 0) {
+    // ---- scale copies and MMAs
+    uint32_t it = 0, acc_it = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step, ++acc_it) {
+      const int n0 = (t / p.m_tiles) * NT;
+      const uint32_t shift = (n0 & 127) / 32;  // the tile's first scale column
+      const int acc = acc_it % P::kAccs;
+      ok = wait(&acc_empty[acc], ((acc_it / P::kAccs) & 1) ^ 1, kSitePipeAcc);
+      tc_fence_after_sync();
+      const uint32_t d = tmem + acc * NT;
+      for (int s = s0; s < s1 && ok; ++s, ++it) {
+        const int slot = it % P::kStages;
+        ok = wait(&full[slot], (it / P::kStages) & 1, kSitePipeFull);
+        // the scale columns' last readers: the MMAs kScaleBufs stages ago
+        if (ok && P::kScaleBufs < P::kStages && it >= P::kScaleBufs) {
+          const uint32_t old = it - P::kScaleBufs;
+          ok = wait(&empty[old % P::kStages], (old / P::kStages) & 1, kSitePipeEmpty);
+        }
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t base = smem_addr(stages + slot * P::kStage);
+        const uint32_t sa = base + P::kA + P::kB, sb = sa + P::kSa;
+        const uint32_t ta = scale_tmem + (it % P::kScaleBufs) * P::kScaleCols, tb = ta + P::kTilesK * 4;
+        const int steps = min(kStageK / kStepK, (p.K - s * kStageK + kStepK - 1) / kStepK);
+#pragma unroll
+        for (int c = 0; c < P::kTilesK; ++c) {
+          tmem_copy_scales(ta + c * 4, sa + c * 512);
+#pragma unroll
+          for (int j = 0; j < P::kTilesN; ++j)
+            tmem_copy_scales(tb + (c * P::kTilesN + j) * 4, sb + j * P::kSa + c * 512);
+        }
+        const uint64_t da = umma_desc_sw128_kmajor(base), db = umma_desc_sw128_kmajor(base + P::kA);
+#pragma unroll
+        for (int k = 0; k < kStageK / kStepK; ++k) {
+          if (k >= steps) break;
+          // 64 values: two MXFP4 scales of a word, or all four NVFP4 scales of one
+          const int c = FORMAT == kMxfp4 ? k / 2 : k;
+          const uint32_t sf = FORMAT == kMxfp4 ? (k & 1) * 2 : 0;
+          umma_mx4<FORMAT>(d, da + k * 2, db + k * 2, mx4_idesc<FORMAT>(NT, sf), ta + c * 4,
+                           tb + c * P::kTilesN * 4 + shift, s > s0 || k > 0);
+        }
+        umma_commit(&empty[slot]);
+      }
+      if (ok) umma_commit(&acc_full[acc]);
     }
-    __syncthreads();
+  } else if (warp >= 2) {
+    // ---- results
+    const int quad = warp & 3, half = (warp - 2) >> 2;  // TMEM lanes, half of the columns
+    float scale = p.gw ? *p.gw : 1.0f;
+    if (p.gx) scale *= *p.gx;
+    const bool vec = p.N % (p.y_type == kF32 ? 4 : 8) == 0;
+    uint32_t acc_it = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step, ++acc_it) {
+      const int m0 = (t % p.m_tiles) * kRows, n0 = (t / p.m_tiles) * NT;
+      const int acc = acc_it % P::kAccs;
+      ok = wait(&acc_full[acc], (acc_it / P::kAccs) & 1, kSitePipeAcc);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after_sync();
+      const int row = m0 + quad * 32 + lane;
+      const uint32_t lane_base = tmem + acc * NT + (static_cast<uint32_t>(quad * 32) << 16);
+#pragma unroll 1
+      for (int c = half * (NT / 2); c < (half + 1) * (NT / 2); c += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(lane_base + c, v);
+        const float* f = reinterpret_cast<const float*>(v);
+        if (p.splits > 1) {
+          float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(stages) + (quad * 32 + lane) * P::kRedPitch + c);
 #pragma unroll
-    for (int k = 0; k < kStep; ++k)
+          for (int i = 0; i < 8; ++i) q[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        } else if (row < p.batch) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += As[k][ty * 4 + i] * Bs[k][tx + 16 * j];
-    __syncthreads();
+          for (int i = 0; i < 4; ++i)
+            if (n0 + c + 8 * i < p.N) put8(p, row, n0 + c + 8 * i, f + 8 * i, scale, vec);
+        }
+      }
+      tc_fence_before_sync();
+      mbar_arrive(&acc_empty[acc]);
+    }
   }
-  float scale = w.tensor_scale ? *w.tensor_scale : 1.0f;
-  if (A_TYPE < 0 && a4.tensor_scale) scale *= *a4.tensor_scale;
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int r = i0 + ty * 4 + i, c = j0 + tx + 16 * j;
-      if (r >= rows || c >= cols) continue;
-      const float b = bias ? load_value<OUT_TYPE>(bias, c) : 0.0f;
-      store_value<OUT_TYPE>(out, static_cast<size_t>(r) * cols + c, acc[i][j] * scale + b);
+
+  if (p.splits > 1) {
+    // the partial tiles of the cluster, added in rank order
+    __syncwarp();
+    cluster_sync();
+    const int m0 = (first % p.m_tiles) * kRows, n0 = (first / p.m_tiles) * NT;
+    const int rows = min(kRows, p.batch - m0), cols = min(NT, p.N - n0);
+    const bool vec = p.N % (p.y_type == kF32 ? 4 : 8) == 0;
+    float scale = p.gw ? *p.gw : 1.0f;
+    if (p.gx) scale *= *p.gx;
+    const uint32_t red = smem_addr(stages);
+    for (int e = rank * kThreads + threadIdx.x; e < rows * (NT / 8); e += kThreads * p.splits) {
+      const int r = e / (NT / 8), c = e % (NT / 8) * 8;
+      if (c >= cols) continue;
+      float v[8] = {};
+      for (int s = 0; s < p.splits; ++s) {
+        const uint32_t at = red + (r * P::kRedPitch + c) * 4;
+        const float4 a = ld_cluster_f4(at, s), b = ld_cluster_f4(at + 16, s);
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+      }
+      put8(p, m0 + r, n0 + c, v, scale, vec);
     }
+    cluster_sync();  // no CTA leaves while another reads its partial tile
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, P::kCols);
 }
 
-template <int FORMAT, int A_TYPE, int OUT_TYPE, bool GRAD>
-cudaError_t product(const void* a16, const Mx4& a4, const Mx4& w, const void* bias, void* out, int rows, int cols,
-                    int depth, int K, cudaStream_t stream) {
-  const dim3 grid((cols + kTile - 1) / kTile, (rows + kTile - 1) / kTile);
-  return launch_overlapped(product_kernel<FORMAT, A_TYPE, OUT_TYPE, GRAD>, grid, 256, 0, stream, 1, a16, a4, w, bias,
-                           out, rows, cols, depth, K);
+// Packed rows as a 2-D map of bytes: boxes of 128 bytes x `box` rows, 128-byte swizzle.
+cudaError_t packed_map(CUtensorMap* map, const Mx4& t, int K, int box) {
+  EncodeTiledFn encode = encode_tiled();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(t.rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
+  const cuuint32_t boxes[2] = {kRowBytes, static_cast<cuuint32_t>(box)};
+  const cuuint32_t ones[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(t.packed), dims, strides, boxes, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+constexpr int kSms = 148;
+
+template <int FORMAT, int NT>
+cudaError_t product_as(const Mx4Product& p, int splits, uint32_t* status, cudaStream_t stream) {
+  using P = Plan<FORMAT, NT>;
+  CUtensorMap x_map, w_map;
+  cudaError_t e = packed_map(&x_map, p.x, p.K, kRows);
+  if (e == cudaSuccess) e = packed_map(&w_map, p.w, p.K, NT);
+  if (e != cudaSuccess) return e;
+  ProductParams q{};
+  q.xs = p.x.scales;
+  q.ws = p.w.scales;
+  q.gx = p.x.tensor_scale;
+  q.gw = p.w.tensor_scale;
+  q.bias = p.bias;
+  q.y = p.y;
+  q.status = status;
+  q.batch = p.x.rows;
+  q.N = p.w.rows;
+  q.K = p.K;
+  q.tiles = mx4_scale_tiles(p.K, FORMAT);
+  q.m_tiles = (q.batch + kRows - 1) / kRows;
+  q.n_tiles = (q.N + NT - 1) / NT;
+  q.splits = splits;
+  q.y_type = p.y_type;
+  auto* kernel = product_kernel<FORMAT, NT>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(P::kSmem));
+  if (e != cudaSuccess) return e;
+  const long long tiles = static_cast<long long>(q.m_tiles) * q.n_tiles;
+  if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const unsigned grid = splits > 1 ? static_cast<unsigned>(tiles * splits) : static_cast<unsigned>(tiles < kSms ? tiles : kSms);
+  return launch_overlapped(kernel, grid, kThreads, P::kSmem, stream, splits, x_map, w_map, q);
+}
+
+// Tile width and K split.  A tile's time is its MMAs (2 cycles per feature and 64 values
+// of K at a rate of 128 x 256 x 64 in 128 cycles) or its loads, plus filling and draining.
+template <int FORMAT>
+cudaError_t product_planned(const Mx4Product& p, uint32_t* status, cudaStream_t stream) {
+  const long long m_tiles = (p.x.rows + kRows - 1) / kRows;
+  const int k_stages = (p.K + kStageK - 1) / kStageK;
+  int best_nt = 256, best_split = 1;
+  double best = 1e300;
+  for (int nt : {64, 128, 192, 256}) {
+    const long long tiles = m_tiles * ((p.w.rows + nt - 1) / nt);
+    for (int split : {1, 2, 4, 8}) {
+      if (split > 1 && (tiles * split > kSms || k_stages < 2 * split || nt > 128)) continue;
+      const double waves = static_cast<double>((tiles * split + kSms - 1) / kSms);
+      const double stages = static_cast<double>((k_stages + split - 1) / split);
+      const double stage = 4 * (nt < 128 ? 64.0 : nt / 2.0);
+      const double drain = nt * 6.0, fill = 2500 + (split > 1 ? 1500 : 0);
+      const double cost = waves * (stages * stage + (nt == 256 ? drain : 0)) + drain + fill;
+      if (cost < best) best = cost, best_nt = nt, best_split = split;
+    }
+  }
+  switch (best_nt) {
+    case 64: return product_as<FORMAT, 64>(p, best_split, status, stream);
+    case 128: return product_as<FORMAT, 128>(p, best_split, status, stream);
+    case 192: return product_as<FORMAT, 192>(p, best_split, status, stream);
+    default: return product_as<FORMAT, 256>(p, best_split, status, stream);
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_mx4_linear(const Mx4Linear& p, uint32_t*, cudaStream_t stream) {
-#define MX4_CASE(f, t) \
-  if (p.format == f && p.type == t) \
-    return product<f, t, t, false>(p.x, Mx4{}, p.w, p.bias, p.y, p.batch, p.w.rows, p.K, p.K, stream);
-  MX4_CASE(kMxfp4, kF16) MX4_CASE(kMxfp4, kBf16) MX4_CASE(kNvfp4, kF16) MX4_CASE(kNvfp4, kBf16)
-#undef MX4_CASE
-  return cudaErrorInvalidValue;
-}
-
-cudaError_t launch_mx4_product(const Mx4Product& p, uint32_t*, cudaStream_t stream) {
-#define MX4_CASE(f, t) \
-  if (p.format == f && p.y_type == t) \
-    return product<f, -1, t, false>(nullptr, p.x, p.w, p.bias, p.y, p.x.rows, p.w.rows, p.K, p.K, stream);
-  MX4_CASE(kMxfp4, kF16) MX4_CASE(kMxfp4, kBf16) MX4_CASE(kMxfp4, kF32)
-  MX4_CASE(kNvfp4, kF16) MX4_CASE(kNvfp4, kBf16) MX4_CASE(kNvfp4, kF32)
-#undef MX4_CASE
-  return cudaErrorInvalidValue;
-}
-
-cudaError_t launch_mx4_grad(const Mx4Grad& p, uint32_t*, cudaStream_t stream) {
-#define MX4_CASE(f, t) \
-  if (p.format == f && p.type == t) \
-    return product<f, t, t, true>(p.dy, Mx4{}, p.w, nullptr, p.dx, p.batch, p.K, p.w.rows, p.K, stream);
-  MX4_CASE(kMxfp4, kF16) MX4_CASE(kMxfp4, kBf16) MX4_CASE(kNvfp4, kF16) MX4_CASE(kNvfp4, kBf16)
-#undef MX4_CASE
-  return cudaErrorInvalidValue;
+cudaError_t launch_mx4_product(const Mx4Product& p, uint32_t* status, cudaStream_t stream) {
+  return p.format == kMxfp4 ? product_planned<kMxfp4>(p, status, stream) : product_planned<kNvfp4>(p, status, stream);
 }
 
 }  // namespace aqlm
