@@ -296,6 +296,25 @@ def test_input_grad_exact(dev, fmt, dtype, N, K):
 
 @pytest.mark.parametrize("fmt", [MX, NV])
 @pytest.mark.parametrize("dtype", TYPES[:2])
+@pytest.mark.parametrize("batch", [130, 256, 257, 700])
+def test_products_over_many_features_exact(dev, fmt, dtype, batch):
+    """Enough output tiles to fill the device, with a last one of few features."""
+    w, W = whole(9500, 544, fmt, 17, dev)
+    x = torch.randint(-3, 4, (batch, 544), generator=gen(batch, 3)).to(dtype)
+    assert torch.equal(mx4.matmul(x.to(dev), w).cpu(), once(x.double() @ W.T, dtype))
+    q, X = whole(batch, 544, fmt, 18, dev)
+    assert torch.equal(mx4.matmul(q, w, out_dtype=dtype).cpu(), once(X @ W.T, dtype))
+    w, W = whole(600, 9504, fmt, 19, dev)
+    dy = torch.randint(-2, 3, (batch, 600), generator=gen(batch, 4)).to(dtype)
+    assert torch.equal(mx4.input_grad(dy.to(dev), w).cpu(), once(dy.double() @ W, dtype))
+    w, W = whole(601, 9504, fmt, 19, dev)
+    dy = torch.randint(-2, 3, (batch, 601), generator=gen(batch, 4)).to(dtype)
+    assert torch.equal(mx4.input_grad(dy.to(dev), w).cpu(), once(dy.double() @ W, dtype))
+    status_ok()
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("dtype", TYPES[:2])
 @pytest.mark.parametrize("batch,N,K", [(1, 1024, 4096), (5, 500, 2080), (40, 384, 4096), (300, 700, 1024)])
 def test_products_of_ordinary_values(dev, fmt, dtype, batch, N, K):
     w, W = ordinary(N, K, fmt, 9, dev)

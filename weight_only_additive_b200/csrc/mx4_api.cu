@@ -102,7 +102,7 @@ aqlm_status mx4_dequantize(const void* packed, const void* scales, const void* t
 
 size_t mx4_matmul_workspace_size(mx4_type type, long long N, long long K, long long batch, mx4_format format) {
   if (!rows_ok(N) || !rows_ok(batch) || !K_ok(K) || !format_ok(format) || !type16(type)) return 0;
-  return 0;
+  return aqlm::mx4_linear_workspace(type, format, K, batch);
 }
 
 aqlm_status mx4_matmul(const void* x, mx4_type type, const void* w_packed, const void* w_scales,
@@ -154,7 +154,7 @@ aqlm_status mx4_matmul_mx4(const void* x_packed, const void* x_scales, const voi
 
 size_t mx4_input_grad_workspace_size(mx4_type type, long long N, long long K, long long batch, mx4_format format) {
   if (!rows_ok(N) || !rows_ok(batch) || !K_ok(K) || !format_ok(format) || !type16(type)) return 0;
-  return 0;
+  return aqlm::mx4_grad_workspace(type, format, N, batch);
 }
 
 aqlm_status mx4_input_grad(const void* dy, mx4_type type, const void* w_packed, const void* w_scales,

@@ -41,6 +41,7 @@ struct Mx4Linear {
   void* workspace;
 };
 cudaError_t launch_mx4_linear(const Mx4Linear& p, uint32_t* status, cudaStream_t stream);
+size_t mx4_linear_workspace(int type, int format, long long K, long long batch);
 
 // y = x . W^T with both operands in 4 bits.
 struct Mx4Product {
@@ -62,6 +63,7 @@ struct Mx4Grad {
   void* workspace;
 };
 cudaError_t launch_mx4_grad(const Mx4Grad& p, uint32_t* status, cudaStream_t stream);
+size_t mx4_grad_workspace(int type, int format, long long N, long long batch);
 
 // Device address of the library's status word on the current device (null on failure).
 uint32_t* status_word();

@@ -1,95 +1,640 @@
-// Products with a 4-bit weight matrix: 64 x 64 output tiles, both operands decoded to
-// fp32 in shared memory, 4 x 4 outputs a thread.
+// Products of 16-bit activations with a microscaled 4-bit weight matrix, for more than a
+// few tokens: y = x . W^T + bias and the input gradient dx = dy . W, on the fp16 / bf16
+// tensor-core path with the weights decoded on chip.
+//
+// The MMA's rows (TMEM lanes) are 128 output features a CTA, its columns a tile of up to
+// 256 tokens.  Eight warps decode the weights of a stage (64 values of the reduction)
+// exactly: e2m1 times an e4m3 scale fits fp16 and bf16, e2m1 times a power of two fits
+// bf16.  For y a lane's 64 values go to tensor memory, which takes the decoded operand off
+// the shared-memory ports; for dx, where the reduction runs over weight rows, they go to
+// shared memory with the features contiguous (MN-major).  Packed weights and scales arrive
+// by TMA in a ring of 256-deep slots, activations in one of 64-deep stages.
+//
+// With many tokens two CTAs form a pair (cta_group::2): 256 features x 256 tokens, each
+// decoding its own 128 features and loading half of the tokens, which halves the L2 traffic
+// that bounds a single CTA's tile.  With few, a cluster of CTAs splits the reduction and
+// adds the fp32 partial tiles through distributed shared memory in rank order.
+//
+// fp16 activations with MXFP4 weights fit neither type together: x is split into two bf16
+// parts, x = hi + lo exactly (11 bits into 8 + 8), and every stage is multiplied twice.
 #include "mx4_device.cuh"
 
 namespace aqlm {
 namespace {
 
-constexpr int kTile = 64, kStep = 32;
+constexpr int kF = 128;          // features of a CTA
+constexpr int kDepth = 64;       // reduction depth of a stage
+constexpr int kSlotDepth = 256;  // and of a weight slot
+constexpr int kSlotStages = kSlotDepth / kDepth;
+constexpr int kABytes = kF * kDepth * 2;
+constexpr int kSlotBytes = 16384, kSlotScales = 2048;
+constexpr int kDone = 8;         // ring of stage-completion barriers
+constexpr int kWarpX = 0, kWarpMma = 1, kWarpDecode = 2, kWarpOut = 10, kWarpW = 14;
+constexpr int kThreads = 15 * 32;
+constexpr int kSms = 148;
 
-// Value (r, k) of a 4-bit tensor, its tensor scale left out.
-template <int FORMAT>
-__device__ __forceinline__ float mx4_value(const Mx4& t, int r, int k, int K, int tiles) {
-  const uint32_t byte = t.packed[static_cast<size_t>(r) * (K / 2) + k / 2];
-  uint32_t h[4];
-  e2m1x8_to_f16(byte >> ((k & 1) * 4), h);
-  return h2_to_f2(h[0]).x * mx4_scale_value<FORMAT>(t.scales[mx4_scale_at(r, k / mx4_block(FORMAT), tiles)]);
+template <bool GRAD>
+struct Shape {
+  static constexpr int kASlots = GRAD ? 4 : 8;  // in shared memory / in TMEM
+  static constexpr int kWSlots = GRAD ? 3 : 4;
+  static constexpr int kXBytes = (GRAD ? 96 : 128) * 1024;
+  static constexpr int kA = 0;
+  static constexpr int kX = GRAD ? kASlots * kABytes : 0;
+  static constexpr int kW = kX + kXBytes;
+  static constexpr int kS = kW + kWSlots * kSlotBytes;
+  static constexpr size_t kSmem = kS + kWSlots * kSlotScales + 1024;
+  static constexpr uint32_t kATmem = 256;  // TMEM columns of the decoded stages (not GRAD)
+};
+
+struct LinearParams {
+  const uint8_t* scales;
+  const float* gamma;
+  const void* bias;
+  void* out;
+  uint32_t* status;
+  int features, depth, batch;  // of the output, of the reduction
+  int tiles;                   // scale tiles along K
+  int nt, f_tiles, t_tiles;    // tokens of a tile; tiles
+  int splits, parts, x_stages, out_type;
+};
+
+// Instruction descriptor of kind::f16 with fp32 sums; bit 15: A is MN-major.
+template <int TYPE, bool GRAD>
+__device__ __forceinline__ uint32_t linear_idesc(uint32_t m, uint32_t n) {
+  const uint32_t t = TYPE == kBf16 ? 1u : 0u;
+  return 1u << 4 | t << 7 | t << 10 | (GRAD ? 1u << 15 : 0u) | (n >> 3) << 17 | (m >> 4) << 24;
 }
 
-// out[i][j] = sum_k a(i, k) b(j, k): a from 16-bit rows (A_TYPE) or a 4-bit tensor (-1),
-// b the weight (GRAD: its transpose).
-template <int FORMAT, int A_TYPE, int OUT_TYPE, bool GRAD>
-__global__ void __launch_bounds__(256) product_kernel(const void* a16, Mx4 a4, Mx4 w, const void* bias, void* out,
-                                                      int rows, int cols, int depth, int K) {
-  __shared__ float As[kStep][kTile + 1], Bs[kStep][kTile + 1];
+template <int CG>
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 1)
+    umma_f16_ss(d, a, b, idesc, accumulate);
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 1)
+    umma_f16_ts(d, a, b, idesc, accumulate);
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// MN-major 128-byte-swizzled stage: 64 reduction rows of 128 features; atoms of 8 rows x
+// 64 features (1 KB), 8-row groups 1024 bytes apart, feature halves 8192.
+__device__ __forceinline__ uint32_t mn_offset(int n, int chunk) {
+  return static_cast<uint32_t>((chunk >> 3) * 8192 + (n >> 3) * 1024 + (n & 7) * 128 + (((chunk & 7) ^ (n & 7)) << 4));
+}
+__device__ __forceinline__ uint64_t mn_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | static_cast<uint64_t>(8192u >> 4) << 16 |
+         static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// What decoded pairs are multiplied by for a block whose scale byte is `b`.
+//   fp16: the scale.  bf16: the scale times 2^112, as the pairs arrive as fp16 bits moved
+//   three places down, which divides them by 2^112; a power of two above 2^15 is then out
+//   of range and comes in two factors.
+template <int FORMAT, int TYPE>
+struct Scale {
+  uint32_t pair;
+  uint32_t more;  // MXFP4: the second factor, or 0
+
+  __device__ __forceinline__ explicit Scale(uint32_t b) {
+    more = 0;
+    if constexpr (FORMAT == kMxfp4) {
+      const uint32_t e = b == 255 ? 0x7FC0u : min(b + 112u, 254u) << 7;
+      pair = e * 0x10001u;
+      if (b > 142 && b != 255) more = ((b - 142 + 127) << 7) * 0x10001u;
+    } else if constexpr (TYPE == kF16) {
+      uint32_t h;
+      asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(b | b << 8));
+      pair = h;
+    } else {
+      const uint32_t f = __float_as_uint(mx4_scale_value<kNvfp4>(b) * 0x1p112f) >> 16;
+      pair = f * 0x10001u;
+    }
+  }
+  // eight codes to four pairs
+  __device__ __forceinline__ void apply(uint32_t codes, uint32_t (&h)[4]) const {
+    e2m1x8_to_f16(codes, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (TYPE == kF16) {
+        h[i] = hmul2(h[i], pair);
+      } else {
+        const uint32_t t = ((h[i] & 0x7FFF7FFFu) >> 3) | (h[i] & 0x80008000u);
+        h[i] = bmul2(t, pair);
+      }
+    }
+    if (FORMAT == kMxfp4 && more) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = bmul2(h[i], more);
+    }
+  }
+};
+
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
+      "tcgen05.wait::st.sync.aligned;"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+template <int FORMAT, int TYPE, bool GRAD, int CG>
+__global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ CUtensorMap x_map,
+                                                             const __grid_constant__ CUtensorMap w_map,
+                                                             const LinearParams p) {
+  using S = Shape<GRAD>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t smem = (smem_addr(smem_raw) + 1023) & ~1023u;
+  uint8_t* smem_ptr = smem_raw + (smem - smem_addr(smem_raw));
+  __shared__ uint64_t x_full[kDone], peer_full[kDone], a_full[S::kASlots], done[kDone], w_full[S::kWSlots],
+      w_empty[S::kWSlots], acc_full[2], acc_empty[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t failed;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG > 1 || p.splits > 1 ? static_cast<int>(cluster_rank()) : 0;
+  if (threadIdx.x == 0) {
+    failed = 0;
+    for (int i = 0; i < kDone; ++i) {
+      mbar_init(&x_full[i], 1);
+      mbar_init(&peer_full[i], 1);
+      mbar_init(&done[i], 1);
+    }
+    for (int i = 0; i < S::kASlots; ++i) mbar_init(&a_full[i], 4 * CG);
+    for (int i = 0; i < S::kWSlots; ++i) {
+      mbar_init(&w_full[i], 1);
+      mbar_init(&w_empty[i], 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4 * CG);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kWarpMma) tmem_alloc_cg<CG>(&tmem_slot, 512);
+  tc_fence_before_sync();
+  __syncthreads();
+  if (CG > 1) cluster_sync();  // the pair's barriers are ready before either arrives on them
+  tc_fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+
   grid_dependency_wait();
   grid_dependents_launch();
-  const int tiles = (K / mx4_block(FORMAT) + 3) / 4;
-  const int i0 = blockIdx.y * kTile, j0 = blockIdx.x * kTile, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < depth; k0 += kStep) {
-    for (int e = threadIdx.x; e < kTile * kStep; e += 256) {
-      const int i = e / kStep, k = e % kStep;
-      float v = 0.0f;
-      if (i0 + i < rows && k0 + k < depth) {
-        if constexpr (A_TYPE >= 0) v = load_value<A_TYPE>(a16, static_cast<size_t>(i0 + i) * depth + k0 + k);
-        else v = mx4_value<FORMAT>(a4, i0 + i, k0 + k, K, tiles);
+
+  const int slots = (p.depth + kSlotDepth - 1) / kSlotDepth;
+  const int k_rank = CG > 1 ? 0 : rank;
+  const int s0 = slots * k_rank / p.splits, s1 = slots * (k_rank + 1) / p.splits;
+  const int total = p.f_tiles * p.t_tiles;
+  const int per = CG > 1 ? CG : p.splits;
+  const int first = blockIdx.x / per, step = gridDim.x / per;
+  const int accs = GRAD || p.nt <= 128 ? 2 : 1;
+  const uint32_t acc_cols = GRAD ? 256 : 128;
+  const uint32_t x_part = static_cast<uint32_t>(p.nt / CG) * 128, x_stage = x_part * p.parts;
+  const auto features_at = [&](int t) { return (t / p.t_tiles) * kF * CG + (CG > 1 ? rank * kF : 0); };
+  const auto tokens_at = [&](int t) { return (t % p.t_tiles) * p.nt; };
+  const auto stages_of = [&](int s) { return min(kSlotStages, (p.depth - s * kSlotDepth + kDepth - 1) / kDepth); };
+  // a wait that gives up makes every later one in this CTA end at once
+  const auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+    if (failed) return false;
+    if (mbar_wait_bounded(bar, parity, p.status, site)) return true;
+    failed = 1;
+    return false;
+  };
+  const auto wait_pair = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+    if constexpr (CG == 1) return wait(bar, parity, site);
+    if (failed) return false;
+    if (mbar_wait_cluster(bar, parity, p.status, site)) return true;
+    failed = 1;
+    return false;
+  };
+  // stage i - back has been multiplied
+  const auto wait_done = [&](uint32_t i, uint32_t back) {
+    return i < back || wait(&done[(i - back) % kDone], ((i - back) / kDone) & 1, kSitePipeEmpty);
+  };
+  const auto arrive_pair = [&](uint64_t* bar) {
+    if constexpr (CG == 1) mbar_arrive(bar);
+    else mbar_arrive_leader(bar);
+  };
+
+  if (warp == kWarpX && lane == 0) {
+    // ---- activations
+    const uint64_t keep = l2_policy_evict_last();
+    uint32_t i = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step) {
+      const int row = tokens_at(t) + (CG > 1 ? rank * (p.nt / CG) : 0);
+      for (int s = s0; s < s1 && ok; ++s)
+        for (int j = 0, n = stages_of(s); j < n; ++j, ++i) {
+          ok = wait_done(i, p.x_stages);
+          if (!ok) break;
+          const uint32_t slot = i % p.x_stages, at = smem + S::kX + slot * x_stage;
+          mbar_arrive_expect_tx(&x_full[slot], x_stage);
+          for (int q = 0; q < p.parts; ++q)
+            tma_load_2d(at + q * x_part, &x_map, s * kSlotDepth + j * kDepth, row + q * p.batch, &x_full[slot], keep);
+        }
+    }
+    if (!ok)  // copies still in flight land before the shared memory goes away
+      for (uint32_t j = i > static_cast<uint32_t>(p.x_stages) ? i - p.x_stages : 0; j < i; ++j)
+        mbar_wait_bounded(&x_full[j % p.x_stages], (j / p.x_stages) & 1, p.status, kSitePipeFull);
+  } else if (warp == kWarpW && lane == 0) {
+    // ---- packed weights and scales
+    const uint64_t pol = p.t_tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+    const int row_tiles = ((GRAD ? p.depth : p.features) + 127) / 128;
+    uint32_t i = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step) {
+      const int f0 = features_at(t);
+      for (int s = s0; s < s1; ++s, ++i) {
+        const uint32_t slot = i % S::kWSlots;
+        ok = wait(&w_empty[slot], ((i / S::kWSlots) & 1) ^ 1, kSitePipeCodes);
+        if (!ok) break;
+        const uint32_t at = smem + S::kW + slot * kSlotBytes, sc = smem + S::kS + slot * kSlotScales;
+        // scale tiles: along K (y), or those of the CTA's features in two row tiles (dx)
+        const int c0 = GRAD ? f0 / (4 * mx4_block(FORMAT)) : s * kSlotDepth / (4 * mx4_block(FORMAT));
+        const int most = (GRAD ? kF : kSlotDepth) / (4 * mx4_block(FORMAT));
+        const int r0 = GRAD ? s * 2 : f0 / 128, r_most = GRAD ? 2 : 1;
+        // a pair's second CTA may have no features: its rows are read as zeros
+        const uint32_t run = static_cast<uint32_t>(max(0, min(most, p.tiles - c0))) * 512;
+        const int rows = run ? max(0, min(r_most, row_tiles - r0)) : 0;
+        mbar_arrive_expect_tx(&w_full[slot], kSlotBytes + rows * run);
+        if constexpr (GRAD) tma_load_2d(at, &w_map, f0 / 2, s * kSlotDepth, &w_full[slot], pol);
+        else tma_load_2d(at, &w_map, s * (kSlotDepth / 2), f0, &w_full[slot], pol);
+        for (int r = 0; r < rows; ++r)
+          bulk_load(sc + r * (kSlotScales / 2), p.scales + (static_cast<size_t>(r0 + r) * p.tiles + c0) * 512, run,
+                    &w_full[slot]);
       }
-      As[k][i] = v;
     }
-    for (int e = threadIdx.x; e < kTile * kStep; e += 256) {
-      const int j = GRAD ? e % kTile : e / kStep, k = GRAD ? e / kTile : e % kStep;
-      float v = 0.0f;
-      if (j0 + j < cols && k0 + k < depth)
-        v = GRAD ? mx4_value<FORMAT>(w, k0 + k, j0 + j, K, tiles) : mx4_value<FORMAT>(w, j0 + j, k0 + k, K, tiles);
-      Bs[k][j] = v;
+    if (!ok)
+      for (uint32_t j = i > S::kWSlots ? i - S::kWSlots : 0; j < i; ++j)
+        mbar_wait_bounded(&w_full[j % S::kWSlots], (j / S::kWSlots) & 1, p.status, kSitePipeFull);
+  } else if (warp == kWarpMma && lane == 0 && CG > 1 && rank > 0) {
+    // ---- the pair's second CTA tells the first when its activations are there
+    uint32_t i = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step)
+      for (int s = s0; s < s1 && ok; ++s)
+        for (int j = 0, n = stages_of(s); j < n && ok; ++j, ++i) {
+          ok = wait(&x_full[i % p.x_stages], (i / p.x_stages) & 1, kSitePipeFull);
+          if (ok) mbar_arrive_leader(&peer_full[i % p.x_stages]);
+        }
+  } else if (warp == kWarpMma && lane == 0) {
+    // ---- MMAs
+    const uint32_t idesc = linear_idesc<TYPE, GRAD>(kF * CG, p.nt);
+    uint32_t i = 0, n_acc = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step, ++n_acc) {
+      const uint32_t acc = n_acc % accs;
+      ok = wait_pair(&acc_empty[acc], ((n_acc / accs) & 1) ^ 1, kSitePipeAcc);
+      tc_fence_after_sync();
+      const uint32_t d = tmem + acc * acc_cols;
+      uint32_t go = 0;
+      for (int s = s0; s < s1 && ok; ++s)
+        for (int j = 0, n = stages_of(s); j < n; ++j, ++i) {
+          const uint32_t xs = i % p.x_stages, as = i % S::kASlots;
+          ok = wait(&x_full[xs], (i / p.x_stages) & 1, kSitePipeFull);
+          if (CG > 1 && ok) ok = wait_pair(&peer_full[xs], (i / p.x_stages) & 1, kSitePipeFull);
+          if (ok) ok = wait_pair(&a_full[as], (i / S::kASlots) & 1, kSitePipeFull);
+          if (!ok) break;
+          tc_fence_after_sync();
+          for (int q = 0; q < p.parts; ++q) {
+            const uint64_t b = umma_desc_sw128_kmajor(smem + S::kX + xs * x_stage + q * x_part);
+#pragma unroll
+            for (int k = 0; k < kDepth / 16; ++k) {
+              if constexpr (GRAD)
+                umma_ss<CG>(d, mn_desc(smem + S::kA + as * kABytes + k * 2048), b + k * 2, idesc, go);
+              else
+                umma_ts<CG>(d, tmem + S::kATmem + as * 32 + k * 8, b + k * 2, idesc, go);
+              go = 1;
+            }
+          }
+          umma_commit_cg<CG>(&done[i % kDone]);
+        }
+      if (ok) umma_commit_cg<CG>(&acc_full[acc]);
     }
-    __syncthreads();
+  } else if (warp >= kWarpDecode && warp < kWarpOut) {
+    // ---- decoding: two groups of four warps, taking stages in turn
+    const int group = (warp - kWarpDecode) >> 2, quad = warp & 3;
+    const int tid = quad * 32 + lane;
+    uint32_t i = 0, slot_i = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step)
+      for (int s = s0; s < s1 && ok; ++s, ++slot_i) {
+        const uint32_t slot = slot_i % S::kWSlots;
+        ok = __all_sync(0xFFFFFFFFu, wait(&w_full[slot], (slot_i / S::kWSlots) & 1, kSitePipeCodes));
+        if (!ok) break;
+        const uint32_t at = smem + S::kW + slot * kSlotBytes, sc = smem + S::kS + slot * kSlotScales;
+        const int n = stages_of(s);
+        for (int j = 0; j < n; ++j, ++i) {
+          if ((i & 1) != static_cast<uint32_t>(group)) continue;
+          const uint32_t as = i % S::kASlots;
+          ok = __all_sync(0xFFFFFFFFu, wait_done(i, S::kASlots));
+          if (!ok) break;
+          if constexpr (GRAD) {
+            // weight row nl of the stage, 64 of its 128 features: eight lanes of a phase
+            // have eight rows, so their 16-byte stores hit all banks
+            const int nl = tid & 63, half = tid >> 6, row = j * kDepth + nl;
+            const uint32_t base = at + row * 64, turn = (row >> 1) & 3;
+            const uint4 w0 = lds128(base + (((2 * half) ^ turn) << 4)), w1 = lds128(base + (((2 * half + 1) ^ turn) << 4));
+            const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            const uint32_t chunk = FORMAT == kMxfp4 ? 0 : half;
+            uint32_t four = lds32(sc + (row >> 7) * (kSlotScales / 2) + chunk * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4);
+            if (FORMAT == kMxfp4) four >>= half * 16;
+            const bool real = s * kSlotDepth + row < p.depth;  // scales of rows past the end may be anything
+            uint8_t* a = smem_ptr + S::kA + as * kABytes;
+            constexpr int kWords = mx4_block(FORMAT) / 8;  // words of a block
 #pragma unroll
-    for (int k = 0; k < kStep; ++k)
+            for (int b = 0; b < 8 / kWords; ++b) {
+              Scale<FORMAT, TYPE> scale(four >> (8 * b) & 0xFF);
+              if (!real) scale.pair = scale.more = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+              for (int k = 0; k < kWords; ++k) {
+                uint32_t h[4];
+                scale.apply(words[b * kWords + k], h);
+                *reinterpret_cast<uint4*>(a + mn_offset(nl, half * 8 + b * kWords + k)) = make_uint4(h[0], h[1], h[2], h[3]);
+              }
+            }
+            fence_proxy_async_smem();
+          } else {
+            // lane = feature: 64 values of its row
+            const uint32_t base = at + tid * 128;
+            const uint4 w0 = lds128(base + (((2 * j) ^ (tid & 7)) << 4)), w1 = lds128(base + (((2 * j + 1) ^ (tid & 7)) << 4));
+            const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            uint32_t four = lds32(sc + (FORMAT == kMxfp4 ? j >> 1 : j) * 512 + lane * 16 + quad * 4);
+            if (FORMAT == kMxfp4) four >>= (j & 1) * 16;
+            uint32_t out[32];
+            constexpr int kWords = mx4_block(FORMAT) / 8;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += As[k][ty * 4 + i] * Bs[k][tx + 16 * j];
-    __syncthreads();
+            for (int b = 0; b < 8 / kWords; ++b) {
+              const Scale<FORMAT, TYPE> scale(four >> (8 * b) & 0xFF);
+#pragma unroll
+              for (int k = 0; k < kWords; ++k)
+                scale.apply(words[b * kWords + k], *reinterpret_cast<uint32_t(*)[4]>(out + (b * kWords + k) * 4));
+            }
+            tmem_st_x32(tmem + S::kATmem + as * 32 + (static_cast<uint32_t>(quad * 32) << 16), out);
+            tc_fence_before_sync();
+          }
+          __syncwarp();
+          if (lane == 0) arrive_pair(&a_full[as]);
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&w_empty[slot]);
+      }
+  } else if (warp >= kWarpOut && warp < kWarpW) {
+    // ---- results
+    const int quad = warp & 3;
+    const float gamma = p.gamma ? *p.gamma : 1.0f;
+    uint32_t n_acc = 0;
+    for (int t = first; t < total; t += step, ++n_acc) {
+      const uint32_t acc = n_acc % accs;
+      if (!__all_sync(0xFFFFFFFFu, wait(&acc_full[acc], (n_acc / accs) & 1, kSitePipeAcc))) break;
+      tc_fence_after_sync();
+      const int f = features_at(t) + quad * 32 + lane, t0 = tokens_at(t);
+      const int tokens = min(p.nt, p.batch - t0);
+      const bool real = f < p.features;
+      float bias = 0.0f;
+      if (p.bias && real) bias = p.out_type == kF16 ? load_value<kF16>(p.bias, f) : load_value<kBf16>(p.bias, f);
+      const uint32_t d = tmem + acc * acc_cols + (static_cast<uint32_t>(quad * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < p.nt; c += 16) {
+        float v[16];
+        tmem_ld_32x32b_x16(d + c, v);
+        if (p.splits > 1) {
+          float* red = reinterpret_cast<float*>(smem_ptr + S::kX) + quad * 32 + lane;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) red[(c + k) * kF] = v[k];
+        } else if (real) {
+          uint16_t* o = static_cast<uint16_t*>(p.out) + static_cast<size_t>(t0 + c) * p.features + f;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            if (c + k >= tokens) break;
+            const float r = fmaf(v[k], gamma, bias);
+            if (p.out_type == kF16) store_value<kF16>(o, static_cast<size_t>(k) * p.features, r);
+            else store_value<kBf16>(o, static_cast<size_t>(k) * p.features, r);
+          }
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive_pair(&acc_empty[acc]);
+    }
   }
-  float scale = w.tensor_scale ? *w.tensor_scale : 1.0f;
-  if (A_TYPE < 0 && a4.tensor_scale) scale *= *a4.tensor_scale;
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int r = i0 + ty * 4 + i, c = j0 + tx + 16 * j;
-      if (r >= rows || c >= cols) continue;
-      const float b = bias ? load_value<OUT_TYPE>(bias, c) : 0.0f;
-      store_value<OUT_TYPE>(out, static_cast<size_t>(r) * cols + c, acc[i][j] * scale + b);
+
+  __syncwarp();
+  if (CG == 1 && p.splits > 1) {
+    cluster_sync();
+    const int f0 = features_at(first), t0 = tokens_at(first);
+    const int tokens = min(p.nt, p.batch - t0);
+    const float gamma = p.gamma ? *p.gamma : 1.0f;
+    const uint32_t red = smem + S::kX;
+    for (int e = rank * kThreads + threadIdx.x; e < tokens * (kF / 4); e += kThreads * p.splits) {
+      const int c = e / (kF / 4), k = e % (kF / 4) * 4;
+      float v[4] = {};
+      for (int s = 0; s < p.splits; ++s) {
+        const float4 a = ld_cluster_f4(red + (c * kF + k) * 4, s);
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int f = f0 + k + q;
+        if (f >= p.features) break;
+        const size_t at = static_cast<size_t>(t0 + c) * p.features + f;
+        if (p.out_type == kF16) store_value<kF16>(p.out, at, fmaf(v[q], gamma, p.bias ? load_value<kF16>(p.bias, f) : 0.0f));
+        else store_value<kBf16>(p.out, at, fmaf(v[q], gamma, p.bias ? load_value<kBf16>(p.bias, f) : 0.0f));
+      }
     }
+    cluster_sync();  // no CTA leaves while another reads its partial tile
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (CG > 1) cluster_sync();
+  if (warp == kWarpMma) tmem_dealloc_cg<CG>(tmem, 512);
 }
 
-template <int FORMAT, int A_TYPE, int OUT_TYPE, bool GRAD>
-cudaError_t product(const void* a16, const Mx4& a4, const Mx4& w, const void* bias, void* out, int rows, int cols,
-                    int depth, int K, cudaStream_t stream) {
-  const dim3 grid((cols + kTile - 1) / kTile, (rows + kTile - 1) / kTile);
-  return launch_overlapped(product_kernel<FORMAT, A_TYPE, OUT_TYPE, GRAD>, grid, 256, 0, stream, 1, a16, a4, w, bias,
-                           out, rows, cols, depth, K);
+// Activations laid out for the kernel: rows of `pitch` values (a multiple of 8), copied, or
+// split into two bf16 parts, the second `batch` rows further on.
+template <bool SPLIT>
+__global__ void __launch_bounds__(256) restage_kernel(const uint16_t* __restrict__ x, uint16_t* __restrict__ out,
+                                                      long long total, int cols, int pitch, int batch) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  for (long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; e < total;
+       e += static_cast<long long>(gridDim.x) * 256) {
+    const long long r = e / pitch;
+    const int c = static_cast<int>(e - r * pitch);
+    const uint16_t raw = c < cols ? x[r * cols + c] : 0;
+    if constexpr (SPLIT) {
+      const float v = __half2float(__ushort_as_half(raw));
+      const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+      const float rest = v - __bfloat162float(hi);
+      out[e] = __bfloat16_as_ushort(hi);
+      out[total + e] = __bfloat16_as_ushort(__float2bfloat16_rn(isfinite(v) ? rest : 0.0f));
+    } else {
+      out[e] = raw;
+    }
+  }
+}
+
+struct Call {
+  const void* x;  // [batch, depth]
+  Mx4 w;
+  const void* bias;
+  void* out;
+  int type, features, depth, K, batch, format;
+  void* workspace;
+};
+
+bool split_parts(int type, int format) { return type == kF16 && format == kMxfp4; }
+size_t restaged_bytes(int type, int format, long long depth, long long batch) {
+  if (!split_parts(type, format) && depth % 8 == 0) return 0;
+  return static_cast<size_t>(batch) * ((depth + 7) / 8 * 8) * 2 * (split_parts(type, format) ? 2 : 1);
+}
+
+struct Tiling {
+  int nt, cg, splits;
+};
+
+// Tokens of a tile, pairs and the split of the reduction.  A stage takes its MMAs (nt / 2
+// cycles per 16 values of depth) or at least the decoding.
+Tiling plan(int features, int depth, int batch, int parts) {
+  const int slots = (depth + kSlotDepth - 1) / kSlotDepth;
+  const int most = parts > 1 ? 128 : 256;
+  const int t_tiles = (batch + most - 1) / most;
+  int nt = ((batch + t_tiles - 1) / t_tiles + 15) / 16 * 16;
+  const int f_tiles = (features + kF - 1) / kF;
+  if (batch > 128 && static_cast<long long>(f_tiles + 1) / 2 * t_tiles >= kSms / 4) return {(nt + 31) / 32 * 32, 2, 1};
+  int splits = 1;
+  while (splits < 8 && static_cast<long long>(f_tiles) * t_tiles * splits * 2 <= kSms && slots >= 2 * splits * 2 && nt <= 128)
+    splits *= 2;
+  return {nt, 1, splits};
+}
+
+cudaError_t map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* p, uint64_t cols, uint64_t rows, uint64_t pitch,
+                   uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn encode = encode_tiled();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch};
+  const cuuint32_t box[2] = {box_cols, box_rows}, ones[2] = {1, 1};
+  return encode(map, type, 2, const_cast<void*>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <int FORMAT, int TYPE, bool GRAD, int CG>
+cudaError_t launch_linear(const Call& c, const Tiling& tl, uint32_t* status, cudaStream_t stream) {
+  using S = Shape<GRAD>;
+  const int parts = split_parts(c.type, c.format) ? 2 : 1;
+  const int pitch = (c.depth + 7) / 8 * 8;
+  const void* x = c.x;
+  cudaError_t e;
+  if (restaged_bytes(c.type, c.format, c.depth, c.batch)) {
+    const long long total = static_cast<long long>(c.batch) * pitch;
+    const long long blocks = (total + 255) / 256;
+    auto* out = static_cast<uint16_t*>(c.workspace);
+    e = launch_overlapped(parts > 1 ? restage_kernel<true> : restage_kernel<false>,
+                          static_cast<unsigned>(blocks < kSms * 64 ? blocks : kSms * 64), 256, 0, stream, 1,
+                          static_cast<const uint16_t*>(c.x), out, total, c.depth, pitch, c.batch);
+    if (e != cudaSuccess) return e;
+    x = out;
+  }
+  CUtensorMap x_map, w_map;
+  e = map_2d(&x_map, TYPE == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, c.depth,
+             static_cast<uint64_t>(c.batch) * parts, static_cast<uint64_t>(pitch) * 2, kDepth, tl.nt / CG,
+             CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  e = map_2d(&w_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.w.packed, c.K / 2, c.w.rows, c.K / 2, GRAD ? 64 : 128,
+             GRAD ? 256 : 128, GRAD ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  LinearParams q{};
+  q.scales = c.w.scales;
+  q.gamma = c.w.tensor_scale;
+  q.bias = c.bias;
+  q.out = c.out;
+  q.status = status;
+  q.features = c.features;
+  q.depth = c.depth;
+  q.batch = c.batch;
+  q.tiles = mx4_scale_tiles(c.K, FORMAT);
+  q.nt = tl.nt;
+  q.f_tiles = (c.features + kF * CG - 1) / (kF * CG);
+  q.t_tiles = (c.batch + tl.nt - 1) / tl.nt;
+  q.splits = tl.splits;
+  q.parts = parts;
+  const int stage = tl.nt / CG * 128 * parts;
+  q.x_stages = S::kXBytes / stage < kDone ? S::kXBytes / stage : kDone;
+  q.out_type = c.type;
+  const long long tiles = static_cast<long long>(q.f_tiles) * q.t_tiles;
+  if (tiles > 0x7FFFFFFF / 8) return cudaErrorInvalidValue;
+  auto* kernel = linear_kernel<FORMAT, TYPE, GRAD, CG>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
+  if (e != cudaSuccess) return e;
+  const long long ctas = tiles * CG * tl.splits;
+  const unsigned grid = static_cast<unsigned>(tl.splits > 1 || ctas < kSms ? ctas : kSms);
+  return launch_overlapped(kernel, grid, kThreads, S::kSmem, stream, CG * tl.splits, x_map, w_map, q);
+}
+
+template <bool GRAD>
+cudaError_t run(const Call& c, uint32_t* status, cudaStream_t stream) {
+  const Tiling tl = plan(c.features, c.depth, c.batch, split_parts(c.type, c.format) ? 2 : 1);
+#define MX4_CASE(f, t) \
+  return tl.cg == 2 ? launch_linear<f, t, GRAD, 2>(c, tl, status, stream) : launch_linear<f, t, GRAD, 1>(c, tl, status, stream);
+  if (c.format == kMxfp4) { MX4_CASE(kMxfp4, kBf16) }
+  if (c.type == kF16) { MX4_CASE(kNvfp4, kF16) }
+  MX4_CASE(kNvfp4, kBf16)
+#undef MX4_CASE
 }
 
 }  // namespace
 
-cudaError_t launch_mx4_linear(const Mx4Linear& p, uint32_t*, cudaStream_t stream) {
-#define MX4_CASE(f, t) \
-  if (p.format == f && p.type == t) \
-    return product<f, t, t, false>(p.x, Mx4{}, p.w, p.bias, p.y, p.batch, p.w.rows, p.K, p.K, stream);
-  MX4_CASE(kMxfp4, kF16) MX4_CASE(kMxfp4, kBf16) MX4_CASE(kNvfp4, kF16) MX4_CASE(kNvfp4, kBf16)
-#undef MX4_CASE
-  return cudaErrorInvalidValue;
+size_t mx4_linear_workspace(int type, int format, long long K, long long batch) {
+  return restaged_bytes(type, format, K, batch);
+}
+size_t mx4_grad_workspace(int type, int format, long long N, long long batch) {
+  return restaged_bytes(type, format, N, batch);
 }
 
-cudaError_t launch_mx4_grad(const Mx4Grad& p, uint32_t*, cudaStream_t stream) {
-#define MX4_CASE(f, t) \
-  if (p.format == f && p.type == t) \
-    return product<f, t, t, true>(p.dy, Mx4{}, p.w, nullptr, p.dx, p.batch, p.K, p.w.rows, p.K, stream);
-  MX4_CASE(kMxfp4, kF16) MX4_CASE(kMxfp4, kBf16) MX4_CASE(kNvfp4, kF16) MX4_CASE(kNvfp4, kBf16)
-#undef MX4_CASE
-  return cudaErrorInvalidValue;
+cudaError_t launch_mx4_linear(const Mx4Linear& p, uint32_t* status, cudaStream_t stream) {
+  return run<false>(Call{p.x, p.w, p.bias, p.y, p.type, p.w.rows, p.K, p.K, p.batch, p.format, p.workspace}, status, stream);
+}
+
+cudaError_t launch_mx4_grad(const Mx4Grad& p, uint32_t* status, cudaStream_t stream) {
+  return run<true>(Call{p.dy, p.w, nullptr, p.dx, p.type, p.K, p.w.rows, p.K, p.batch, p.format, p.workspace}, status, stream);
 }
 
 }  // namespace aqlm
