@@ -29,15 +29,34 @@ __device__ __forceinline__ float mx4_scale_value(uint32_t b) {
   }
 }
 
-// Eight e2m1 codes (low four bits first) as four fp16 pairs, in order.
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+// Eight e2m1 codes (low four bits first) as four pairs of fp16 or bf16 values, in order:
+// byte lookups by the magnitude bits (in fp16 the low byte is always 0), the sign from a
+// lookup whose codes with the sign bit repeat the top bit of 0x80.  The conversion
+// instruction for e2m1 runs at 4 lanes a clock and SM (measured: it held the decoding
+// products at 80 % of that pipe); these 15 to 17 logic instructions run at 64.
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+template <int TYPE>
+__device__ __forceinline__ void e2m1x8_decode(uint32_t w, uint32_t (&h)[4]) {
+  constexpr uint32_t kHi0 = TYPE == kF16 ? 0x3E3C3800u : 0x3F3F3F00u, kHi1 = TYPE == kF16 ? 0x46444240u : 0x40404040u;
+  const uint32_t m = w & 0x77777777u;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t mi = m >> (16 * i), wi = w >> (16 * i);
+    const uint32_t sign = prmt(0x80808080u, 0x80808080u, wi);  // 0xFF or 0x80
+    const uint32_t hi = prmt(kHi0, kHi1, mi) | ((sign << 7) & 0x80808080u);
+    if constexpr (TYPE == kF16) {
+      h[2 * i] = prmt(hi, 0, 0x1404);
+      h[2 * i + 1] = prmt(hi, 0, 0x3424);
+    } else {
+      const uint32_t lo = prmt(0xC0800000u, 0xC0804000u, mi);
+      h[2 * i] = prmt(lo, hi, 0x5140);
+      h[2 * i + 1] = prmt(lo, hi, 0x7362);
+    }
+  }
 }
 
 __device__ __forceinline__ float2 b2_to_f2(uint32_t v) {
@@ -95,20 +114,35 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// A wait whose barrier other CTAs of the cluster arrive on.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+// Bounded wait of the pipelined kernels for phase `parity` of `bar` (CLUSTER: other CTAs
+// arrive on it).  The thread sleeps in the barrier unit, up to 10 ms at a time: warps that
+// poll take shared-memory and issue slots from the ones that work (2048 x 4096 x 11008:
+// 350 us polling, 300 us polling with clock reads between).
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
   uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done) : "r"(smem_addr(bar)), "r"(parity), "r"(10000000u) : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done) : "r"(smem_addr(bar)), "r"(parity), "r"(10000000u) : "memory");
   return done != 0;
 }
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t* status, uint32_t site) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
+// `failed` (shared): another wait of this CTA has given up, so this one does too.
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_wait_sleeping(uint64_t* bar, uint32_t parity, uint32_t* status, uint32_t site,
+                                                   volatile uint32_t* failed) {
+  if (mbar_sleep<CLUSTER>(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait_cluster(bar, parity)) {
+  while (!mbar_sleep<CLUSTER>(bar, parity)) {
+    if (*failed) return false;
     if (global_timer_ns() - t0 > kWaitTimeoutNs) {
       record_failure(status, site);
       return false;
@@ -116,6 +150,25 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
   return true;
 }
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// A warp's index as a value that the compiler knows to be the same in all lanes.
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0); }
+
+// Place in a ring of N slots and the parity of the phase that is running there.
+template <int N>
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) slot = 0, phase ^= 1;
+  }
+};
+
 // Arrive on the same barrier of the cluster's CTA 0.
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
   asm volatile(

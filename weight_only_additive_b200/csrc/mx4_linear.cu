@@ -23,28 +23,29 @@ namespace aqlm {
 namespace {
 
 constexpr int kF = 128;          // features of a CTA
-constexpr int kDepth = 64;       // reduction depth of a stage
-constexpr int kSlotDepth = 256;  // and of a weight slot
-constexpr int kSlotStages = kSlotDepth / kDepth;
-constexpr int kABytes = kF * kDepth * 2;
+constexpr int kSlotDepth = 256;  // reduction depth of a weight slot
+constexpr int kRing = 4;         // stages in flight
 constexpr int kSlotBytes = 16384, kSlotScales = 2048;
-constexpr int kDone = 8;         // ring of stage-completion barriers
 constexpr int kWarpX = 0, kWarpMma = 1, kWarpDecode = 2, kWarpOut = 10, kWarpW = 14;
 constexpr int kThreads = 15 * 32;
 constexpr int kSms = 148;
 
 template <bool GRAD>
 struct Shape {
-  static constexpr int kASlots = GRAD ? 4 : 8;  // in shared memory / in TMEM
+  // Reduction depth of a stage.  Every stage costs the MMA thread a wait and a commit, so
+  // deep ones; dx's decoded stages lie in shared memory, which has room for 64.
+  static constexpr int kDepth = GRAD ? 64 : 128;
+  static constexpr int kSlotStages = kSlotDepth / kDepth;
+  static constexpr int kABytes = GRAD ? kF * kDepth * 2 : 0;
+  static constexpr uint32_t kACols = kDepth / 2;  // TMEM columns of a decoded stage (not GRAD)
   static constexpr int kWSlots = GRAD ? 3 : 4;
   static constexpr int kXBytes = (GRAD ? 96 : 128) * 1024;
-  static constexpr int kA = 0;
-  static constexpr int kX = GRAD ? kASlots * kABytes : 0;
+  static constexpr int kX = kRing * kABytes;
   static constexpr int kW = kX + kXBytes;
   static constexpr int kS = kW + kWSlots * kSlotBytes;
   static constexpr size_t kSmem = kS + kWSlots * kSlotScales + 1024;
-  static constexpr uint32_t kATmem = 256;  // TMEM columns of the decoded stages (not GRAD)
 };
+constexpr uint32_t kATmem = 256;  // first TMEM column of the decoded stages
 
 struct LinearParams {
   const uint8_t* scales;
@@ -55,7 +56,7 @@ struct LinearParams {
   int features, depth, batch;  // of the output, of the reduction
   int tiles;                   // scale tiles along K
   int nt, f_tiles, t_tiles;    // tokens of a tile; tiles
-  int splits, parts, x_stages, out_type;
+  int splits, parts, out_type;
 };
 
 // Instruction descriptor of kind::f16 with fp32 sums; bit 15: A is MN-major.
@@ -107,48 +108,29 @@ __device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// What decoded pairs are multiplied by for a block whose scale byte is `b`.
-//   fp16: the scale.  bf16: the scale times 2^112, as the pairs arrive as fp16 bits moved
-//   three places down, which divides them by 2^112; a power of two above 2^15 is then out
-//   of range and comes in two factors.
+// The scale of a block whose scale byte is `b` as a pair of the decoded type (exact).
 template <int FORMAT, int TYPE>
-struct Scale {
-  uint32_t pair;
-  uint32_t more;  // MXFP4: the second factor, or 0
+__device__ __forceinline__ uint32_t scale_pair(uint32_t b) {
+  if constexpr (FORMAT == kMxfp4) {
+    // bf16 exponent field; 2^-127 is subnormal
+    const uint32_t e = b == 255 ? 0x7FC0u : max(b << 7, 0x40u);
+    return e * 0x10001u;
+  } else if constexpr (TYPE == kF16) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(b | b << 8));
+    return h;
+  } else {
+    return (__float_as_uint(mx4_scale_value<kNvfp4>(b)) >> 16) * 0x10001u;
+  }
+}
 
-  __device__ __forceinline__ explicit Scale(uint32_t b) {
-    more = 0;
-    if constexpr (FORMAT == kMxfp4) {
-      const uint32_t e = b == 255 ? 0x7FC0u : min(b + 112u, 254u) << 7;
-      pair = e * 0x10001u;
-      if (b > 142 && b != 255) more = ((b - 142 + 127) << 7) * 0x10001u;
-    } else if constexpr (TYPE == kF16) {
-      uint32_t h;
-      asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(b | b << 8));
-      pair = h;
-    } else {
-      const uint32_t f = __float_as_uint(mx4_scale_value<kNvfp4>(b) * 0x1p112f) >> 16;
-      pair = f * 0x10001u;
-    }
-  }
-  // eight codes to four pairs
-  __device__ __forceinline__ void apply(uint32_t codes, uint32_t (&h)[4]) const {
-    e2m1x8_to_f16(codes, h);
+// Eight codes times the scale as four pairs.
+template <int TYPE>
+__device__ __forceinline__ void decode_scaled(uint32_t codes, uint32_t scale, uint32_t (&h)[4]) {
+  e2m1x8_decode<TYPE>(codes, h);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (TYPE == kF16) {
-        h[i] = hmul2(h[i], pair);
-      } else {
-        const uint32_t t = ((h[i] & 0x7FFF7FFFu) >> 3) | (h[i] & 0x80008000u);
-        h[i] = bmul2(t, pair);
-      }
-    }
-    if (FORMAT == kMxfp4 && more) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = bmul2(h[i], more);
-    }
-  }
-};
+  for (int i = 0; i < 4; ++i) h[i] = TYPE == kF16 ? hmul2(h[i], scale) : bmul2(h[i], scale);
+}
 
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -182,21 +164,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem = (smem_addr(smem_raw) + 1023) & ~1023u;
   uint8_t* smem_ptr = smem_raw + (smem - smem_addr(smem_raw));
-  __shared__ uint64_t x_full[kDone], peer_full[kDone], a_full[S::kASlots], done[kDone], w_full[S::kWSlots],
-      w_empty[S::kWSlots], acc_full[2], acc_empty[2];
+  // ready: a stage's activations (one arrival and their bytes) and its decoded weights (4
+  // warps); the first CTA of a pair also waits for its second's.  done: it is multiplied.
+  __shared__ uint64_t ready[kRing], done[kRing], w_full[S::kWSlots], w_empty[S::kWSlots], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t failed;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int rank = CG > 1 || p.splits > 1 ? static_cast<int>(cluster_rank()) : 0;
   if (threadIdx.x == 0) {
     failed = 0;
-    for (int i = 0; i < kDone; ++i) {
-      mbar_init(&x_full[i], 1);
-      mbar_init(&peer_full[i], 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&ready[i], CG > 1 && rank == 0 ? 6 : 5);
       mbar_init(&done[i], 1);
     }
-    for (int i = 0; i < S::kASlots; ++i) mbar_init(&a_full[i], 4 * CG);
     for (int i = 0; i < S::kWSlots; ++i) {
       mbar_init(&w_full[i], 1);
       mbar_init(&w_empty[i], 8);
@@ -225,66 +206,64 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   const int first = blockIdx.x / per, step = gridDim.x / per;
   const int accs = GRAD || p.nt <= 128 ? 2 : 1;
   const uint32_t acc_cols = GRAD ? 256 : 128;
-  const uint32_t x_part = static_cast<uint32_t>(p.nt / CG) * 128, x_stage = x_part * p.parts;
+  const uint32_t x_box = static_cast<uint32_t>(p.nt / CG) * 128;          // bytes of 64 values of the tile's tokens
+  const uint32_t x_part = x_box * (S::kDepth / 64), x_stage = x_part * p.parts;
   const auto features_at = [&](int t) { return (t / p.t_tiles) * kF * CG + (CG > 1 ? rank * kF : 0); };
   const auto tokens_at = [&](int t) { return (t % p.t_tiles) * p.nt; };
-  const auto stages_of = [&](int s) { return min(kSlotStages, (p.depth - s * kSlotDepth + kDepth - 1) / kDepth); };
-  // a wait that gives up makes every later one in this CTA end at once
+  const auto stages_of = [&](int s) { return min(S::kSlotStages, (p.depth - s * kSlotDepth + S::kDepth - 1) / S::kDepth); };
+  // a wait that gives up makes every later one of this CTA that is not over end soon
   const auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-    if (failed) return false;
-    if (mbar_wait_bounded(bar, parity, p.status, site)) return true;
+    if (mbar_wait_sleeping<false>(bar, parity, p.status, site, &failed)) return true;
     failed = 1;
     return false;
   };
   const auto wait_pair = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-    if constexpr (CG == 1) return wait(bar, parity, site);
-    if (failed) return false;
-    if (mbar_wait_cluster(bar, parity, p.status, site)) return true;
+    if (mbar_wait_sleeping<(CG > 1)>(bar, parity, p.status, site, &failed)) return true;
     failed = 1;
     return false;
   };
-  // stage i - back has been multiplied
-  const auto wait_done = [&](uint32_t i, uint32_t back) {
-    return i < back || wait(&done[(i - back) % kDone], ((i - back) / kDone) & 1, kSitePipeEmpty);
-  };
-  const auto arrive_pair = [&](uint64_t* bar) {
-    if constexpr (CG == 1) mbar_arrive(bar);
-    else mbar_arrive_leader(bar);
-  };
+  // one lane waits for its warp
+  const auto warp_ok = [&](auto&& waits) { return __shfl_sync(0xFFFFFFFFu, lane == 0 ? waits() : false, 0); };
 
   if (warp == kWarpX && lane == 0) {
     // ---- activations
     const uint64_t keep = l2_policy_evict_last();
-    uint32_t i = 0;
+    Ring<kRing> r;
+    uint32_t issued = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
       const int row = tokens_at(t) + (CG > 1 ? rank * (p.nt / CG) : 0);
       for (int s = s0; s < s1 && ok; ++s)
-        for (int j = 0, n = stages_of(s); j < n; ++j, ++i) {
-          ok = wait_done(i, p.x_stages);
+        for (int j = 0, n = stages_of(s); j < n; ++j, r.next(), ++issued) {
+          ok = wait(&done[r.slot], r.phase ^ 1, kSitePipeEmpty);
           if (!ok) break;
-          const uint32_t slot = i % p.x_stages, at = smem + S::kX + slot * x_stage;
-          mbar_arrive_expect_tx(&x_full[slot], x_stage);
+          uint32_t at = smem + S::kX + r.slot * x_stage;
+          mbar_arrive_expect_tx(&ready[r.slot], x_stage);
           for (int q = 0; q < p.parts; ++q)
-            tma_load_2d(at + q * x_part, &x_map, s * kSlotDepth + j * kDepth, row + q * p.batch, &x_full[slot], keep);
+#pragma unroll
+            for (int h = 0; h < S::kDepth / 64; ++h, at += x_box)
+              tma_load_2d(at, &x_map, s * kSlotDepth + j * S::kDepth + h * 64, row + q * p.batch, &ready[r.slot], keep);
         }
     }
-    if (!ok)  // copies still in flight land before the shared memory goes away
-      for (uint32_t j = i > static_cast<uint32_t>(p.x_stages) ? i - p.x_stages : 0; j < i; ++j)
-        mbar_wait_bounded(&x_full[j % p.x_stages], (j / p.x_stages) & 1, p.status, kSitePipeFull);
+    // after a failure what was asked for lands before the shared memory goes away
+    if (!ok && issued) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 1000000) {
+      }
+    }
   } else if (warp == kWarpW && lane == 0) {
     // ---- packed weights and scales
     const uint64_t pol = p.t_tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
     const int row_tiles = ((GRAD ? p.depth : p.features) + 127) / 128;
-    uint32_t i = 0;
+    Ring<S::kWSlots> r;
+    uint32_t issued = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
       const int f0 = features_at(t);
-      for (int s = s0; s < s1; ++s, ++i) {
-        const uint32_t slot = i % S::kWSlots;
-        ok = wait(&w_empty[slot], ((i / S::kWSlots) & 1) ^ 1, kSitePipeCodes);
+      for (int s = s0; s < s1; ++s, r.next(), ++issued) {
+        ok = wait(&w_empty[r.slot], r.phase ^ 1, kSitePipeCodes);
         if (!ok) break;
-        const uint32_t at = smem + S::kW + slot * kSlotBytes, sc = smem + S::kS + slot * kSlotScales;
+        const uint32_t at = smem + S::kW + r.slot * kSlotBytes, sc = smem + S::kS + r.slot * kSlotScales;
         // scale tiles: along K (y), or those of the CTA's features in two row tiles (dx)
         const int c0 = GRAD ? f0 / (4 * mx4_block(FORMAT)) : s * kSlotDepth / (4 * mx4_block(FORMAT));
         const int most = (GRAD ? kF : kSlotDepth) / (4 * mx4_block(FORMAT));
@@ -292,83 +271,93 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         // a pair's second CTA may have no features: its rows are read as zeros
         const uint32_t run = static_cast<uint32_t>(max(0, min(most, p.tiles - c0))) * 512;
         const int rows = run ? max(0, min(r_most, row_tiles - r0)) : 0;
-        mbar_arrive_expect_tx(&w_full[slot], kSlotBytes + rows * run);
-        if constexpr (GRAD) tma_load_2d(at, &w_map, f0 / 2, s * kSlotDepth, &w_full[slot], pol);
-        else tma_load_2d(at, &w_map, s * (kSlotDepth / 2), f0, &w_full[slot], pol);
-        for (int r = 0; r < rows; ++r)
-          bulk_load(sc + r * (kSlotScales / 2), p.scales + (static_cast<size_t>(r0 + r) * p.tiles + c0) * 512, run,
-                    &w_full[slot]);
+        uint64_t* full = &w_full[r.slot];
+        mbar_arrive_expect_tx(full, kSlotBytes + rows * run);
+        if constexpr (GRAD) tma_load_2d(at, &w_map, f0 / 2, s * kSlotDepth, full, pol);
+        else tma_load_2d(at, &w_map, s * (kSlotDepth / 2), f0, full, pol);
+        for (int q = 0; q < rows; ++q)
+          bulk_load(sc + q * (kSlotScales / 2), p.scales + (static_cast<size_t>(r0 + q) * p.tiles + c0) * 512, run, full);
       }
     }
-    if (!ok)
-      for (uint32_t j = i > S::kWSlots ? i - S::kWSlots : 0; j < i; ++j)
-        mbar_wait_bounded(&w_full[j % S::kWSlots], (j / S::kWSlots) & 1, p.status, kSitePipeFull);
-  } else if (warp == kWarpMma && lane == 0 && CG > 1 && rank > 0) {
-    // ---- the pair's second CTA tells the first when its activations are there
-    uint32_t i = 0;
+    if (!ok && issued) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 1000000) {
+      }
+    }
+  } else if (warp == kWarpMma && CG > 1 && rank > 0) {
+    // ---- the pair's second CTA tells the first when its part of a stage is there
+    Ring<kRing> r;
     bool ok = true;
     for (int t = first; t < total && ok; t += step)
       for (int s = s0; s < s1 && ok; ++s)
-        for (int j = 0, n = stages_of(s); j < n && ok; ++j, ++i) {
-          ok = wait(&x_full[i % p.x_stages], (i / p.x_stages) & 1, kSitePipeFull);
-          if (ok) mbar_arrive_leader(&peer_full[i % p.x_stages]);
+        for (int j = 0, n = stages_of(s); j < n && ok; ++j, r.next()) {
+          ok = warp_ok([&] { return wait(&ready[r.slot], r.phase, kSitePipeFull); });
+          if (ok && lane == 0) mbar_arrive_leader(&ready[r.slot]);
         }
-  } else if (warp == kWarpMma && lane == 0) {
-    // ---- MMAs
+  } else if (warp == kWarpMma) {
+    // ---- MMAs: the whole warp walks the stages, so that descriptors stay in uniform
+    // registers; one lane issues
     const uint32_t idesc = linear_idesc<TYPE, GRAD>(kF * CG, p.nt);
-    uint32_t i = 0, n_acc = 0;
+    const bool issuer = elect_one();
+    const uint64_t x_desc = umma_desc_sw128_kmajor(smem + S::kX), a_desc = mn_desc(smem);
+    Ring<kRing> r;
+    uint32_t n_acc = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step, ++n_acc) {
-      const uint32_t acc = n_acc % accs;
-      ok = wait_pair(&acc_empty[acc], ((n_acc / accs) & 1) ^ 1, kSitePipeAcc);
+      const uint32_t acc = accs == 2 ? n_acc & 1 : 0, acc_phase = accs == 2 ? (n_acc >> 1) & 1 : n_acc & 1;
+      ok = wait_pair(&acc_empty[acc], acc_phase ^ 1, kSitePipeAcc);
       tc_fence_after_sync();
       const uint32_t d = tmem + acc * acc_cols;
       uint32_t go = 0;
       for (int s = s0; s < s1 && ok; ++s)
-        for (int j = 0, n = stages_of(s); j < n; ++j, ++i) {
-          const uint32_t xs = i % p.x_stages, as = i % S::kASlots;
-          ok = wait(&x_full[xs], (i / p.x_stages) & 1, kSitePipeFull);
-          if (CG > 1 && ok) ok = wait_pair(&peer_full[xs], (i / p.x_stages) & 1, kSitePipeFull);
-          if (ok) ok = wait_pair(&a_full[as], (i / S::kASlots) & 1, kSitePipeFull);
+        for (int j = 0, n = stages_of(s); j < n; ++j, r.next()) {
+          ok = wait_pair(&ready[r.slot], r.phase, kSitePipeFull);
           if (!ok) break;
           tc_fence_after_sync();
-          for (int q = 0; q < p.parts; ++q) {
-            const uint64_t b = umma_desc_sw128_kmajor(smem + S::kX + xs * x_stage + q * x_part);
+          uint64_t b = x_desc + ((r.slot * x_stage) >> 4);
+          const uint64_t a = a_desc + r.slot * (S::kABytes >> 4);
+          const uint32_t ta = tmem + kATmem + r.slot * S::kACols;
+          if (issuer) {
+            for (int q = 0; q < p.parts; ++q) {
 #pragma unroll
-            for (int k = 0; k < kDepth / 16; ++k) {
-              if constexpr (GRAD)
-                umma_ss<CG>(d, mn_desc(smem + S::kA + as * kABytes + k * 2048), b + k * 2, idesc, go);
-              else
-                umma_ts<CG>(d, tmem + S::kATmem + as * 32 + k * 8, b + k * 2, idesc, go);
-              go = 1;
+              for (int h = 0; h < S::kDepth / 64; ++h, b += x_box >> 4) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  // 16 values: 32 bytes of a swizzled row; of A two 8-row groups, or 8 columns
+                  if constexpr (GRAD) umma_ss<CG>(d, a + k * (2048 >> 4), b + k * 2, idesc, go);
+                  else umma_ts<CG>(d, ta + h * 32 + k * 8, b + k * 2, idesc, go);
+                  go = 1;
+                }
+              }
             }
+            umma_commit_cg<CG>(&done[r.slot]);
           }
-          umma_commit_cg<CG>(&done[i % kDone]);
+          go = 1;
         }
-      if (ok) umma_commit_cg<CG>(&acc_full[acc]);
+      if (ok && issuer) umma_commit_cg<CG>(&acc_full[acc]);
     }
   } else if (warp >= kWarpDecode && warp < kWarpOut) {
     // ---- decoding: two groups of four warps, taking stages in turn
-    const int group = (warp - kWarpDecode) >> 2, quad = warp & 3;
+    const uint32_t group = (warp - kWarpDecode) >> 2, quad = warp & 3;
     const int tid = quad * 32 + lane;
-    uint32_t i = 0, slot_i = 0;
+    Ring<kRing> r;
+    Ring<S::kWSlots> w;
     bool ok = true;
     for (int t = first; t < total && ok; t += step)
-      for (int s = s0; s < s1 && ok; ++s, ++slot_i) {
-        const uint32_t slot = slot_i % S::kWSlots;
-        ok = __all_sync(0xFFFFFFFFu, wait(&w_full[slot], (slot_i / S::kWSlots) & 1, kSitePipeCodes));
+      for (int s = s0; s < s1 && ok; ++s, w.next()) {
+        ok = warp_ok([&] { return wait(&w_full[w.slot], w.phase, kSitePipeCodes); });
         if (!ok) break;
-        const uint32_t at = smem + S::kW + slot * kSlotBytes, sc = smem + S::kS + slot * kSlotScales;
+        const uint32_t at = smem + S::kW + w.slot * kSlotBytes, sc = smem + S::kS + w.slot * kSlotScales;
         const int n = stages_of(s);
-        for (int j = 0; j < n; ++j, ++i) {
-          if ((i & 1) != static_cast<uint32_t>(group)) continue;
-          const uint32_t as = i % S::kASlots;
-          ok = __all_sync(0xFFFFFFFFu, wait_done(i, S::kASlots));
+        for (int j = 0; j < n; ++j, r.next()) {
+          if ((r.slot & 1) != group) continue;
+          ok = warp_ok([&] { return wait(&done[r.slot], r.phase ^ 1, kSitePipeEmpty); });
           if (!ok) break;
+          constexpr int kWords = mx4_block(FORMAT) / 8;  // words of a block
           if constexpr (GRAD) {
             // weight row nl of the stage, 64 of its 128 features: eight lanes of a phase
             // have eight rows, so their 16-byte stores hit all banks
-            const int nl = tid & 63, half = tid >> 6, row = j * kDepth + nl;
+            const int nl = tid & 63, half = tid >> 6, row = j * S::kDepth + nl;
             const uint32_t base = at + row * 64, turn = (row >> 1) & 3;
             const uint4 w0 = lds128(base + (((2 * half) ^ turn) << 4)), w1 = lds128(base + (((2 * half + 1) ^ turn) << 4));
             const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
@@ -376,44 +365,46 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             uint32_t four = lds32(sc + (row >> 7) * (kSlotScales / 2) + chunk * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4);
             if (FORMAT == kMxfp4) four >>= half * 16;
             const bool real = s * kSlotDepth + row < p.depth;  // scales of rows past the end may be anything
-            uint8_t* a = smem_ptr + S::kA + as * kABytes;
-            constexpr int kWords = mx4_block(FORMAT) / 8;  // words of a block
+            uint8_t* a = smem_ptr + r.slot * S::kABytes;
 #pragma unroll
             for (int b = 0; b < 8 / kWords; ++b) {
-              Scale<FORMAT, TYPE> scale(four >> (8 * b) & 0xFF);
-              if (!real) scale.pair = scale.more = 0;
+              const uint32_t scale = real ? scale_pair<FORMAT, TYPE>(four >> (8 * b) & 0xFF) : 0;
 #pragma unroll
               for (int k = 0; k < kWords; ++k) {
                 uint32_t h[4];
-                scale.apply(words[b * kWords + k], h);
+                decode_scaled<TYPE>(words[b * kWords + k], scale, h);
                 *reinterpret_cast<uint4*>(a + mn_offset(nl, half * 8 + b * kWords + k)) = make_uint4(h[0], h[1], h[2], h[3]);
               }
             }
             fence_proxy_async_smem();
           } else {
-            // lane = feature: 64 values of its row
+            // lane = feature: 64 values of its row at a time
             const uint32_t base = at + tid * 128;
-            const uint4 w0 = lds128(base + (((2 * j) ^ (tid & 7)) << 4)), w1 = lds128(base + (((2 * j + 1) ^ (tid & 7)) << 4));
-            const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-            uint32_t four = lds32(sc + (FORMAT == kMxfp4 ? j >> 1 : j) * 512 + lane * 16 + quad * 4);
-            if (FORMAT == kMxfp4) four >>= (j & 1) * 16;
-            uint32_t out[32];
-            constexpr int kWords = mx4_block(FORMAT) / 8;
 #pragma unroll
-            for (int b = 0; b < 8 / kWords; ++b) {
-              const Scale<FORMAT, TYPE> scale(four >> (8 * b) & 0xFF);
+            for (int h = 0; h < S::kDepth / 64; ++h) {
+              const int c = j * (S::kDepth / 64) + h;  // 64 values: 32 bytes, a tile of NVFP4 scales, half an MXFP4 one
+              const uint4 w0 = lds128(base + (((2 * c) ^ (tid & 7)) << 4)), w1 = lds128(base + (((2 * c + 1) ^ (tid & 7)) << 4));
+              const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+              uint32_t four = lds32(sc + (FORMAT == kMxfp4 ? c >> 1 : c) * 512 + lane * 16 + quad * 4);
+              if (FORMAT == kMxfp4) four >>= (c & 1) * 16;
+              const bool real = s * kSlotDepth + c * 64 < p.depth;  // there may be no scales there
+              uint32_t out[32];
 #pragma unroll
-              for (int k = 0; k < kWords; ++k)
-                scale.apply(words[b * kWords + k], *reinterpret_cast<uint32_t(*)[4]>(out + (b * kWords + k) * 4));
+              for (int b = 0; b < 8 / kWords; ++b) {
+                const uint32_t scale = real ? scale_pair<FORMAT, TYPE>(four >> (8 * b) & 0xFF) : 0;
+#pragma unroll
+                for (int k = 0; k < kWords; ++k)
+                  decode_scaled<TYPE>(words[b * kWords + k], scale, *reinterpret_cast<uint32_t(*)[4]>(out + (b * kWords + k) * 4));
+              }
+              tmem_st_x32(tmem + kATmem + r.slot * S::kACols + h * 32 + (quad << 21), out);
             }
-            tmem_st_x32(tmem + S::kATmem + as * 32 + (static_cast<uint32_t>(quad * 32) << 16), out);
             tc_fence_before_sync();
           }
           __syncwarp();
-          if (lane == 0) arrive_pair(&a_full[as]);
+          if (lane == 0) mbar_arrive(&ready[r.slot]);
         }
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&w_empty[slot]);
+        if (ok && lane == 0) mbar_arrive(&w_empty[w.slot]);
       }
   } else if (warp >= kWarpOut && warp < kWarpW) {
     // ---- results
@@ -421,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     const float gamma = p.gamma ? *p.gamma : 1.0f;
     uint32_t n_acc = 0;
     for (int t = first; t < total; t += step, ++n_acc) {
-      const uint32_t acc = n_acc % accs;
-      if (!__all_sync(0xFFFFFFFFu, wait(&acc_full[acc], (n_acc / accs) & 1, kSitePipeAcc))) break;
+      const uint32_t acc = accs == 2 ? n_acc & 1 : 0, acc_phase = accs == 2 ? (n_acc >> 1) & 1 : n_acc & 1;
+      if (!warp_ok([&] { return wait(&acc_full[acc], acc_phase, kSitePipeAcc); })) break;
       tc_fence_after_sync();
       const int f = features_at(t) + quad * 32 + lane, t0 = tokens_at(t);
       const int tokens = min(p.nt, p.batch - t0);
@@ -451,7 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       }
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) arrive_pair(&acc_empty[acc]);
+      if (lane == 0) {
+        if constexpr (CG == 1) mbar_arrive(&acc_empty[acc]);
+        else mbar_arrive_leader(&acc_empty[acc]);
+      }
     }
   }
 
@@ -529,17 +523,23 @@ struct Tiling {
   int nt, cg, splits;
 };
 
-// Tokens of a tile, pairs and the split of the reduction.  A stage takes its MMAs (nt / 2
-// cycles per 16 values of depth) or at least the decoding.
-Tiling plan(int features, int depth, int batch, int parts) {
+// Tokens of a tile, pairs and the split of the reduction.  A CTA's stages hold 128 tokens
+// (192 for dx, whose stages are half as deep), a pair's 256; half of that for two parts.
+Tiling plan(int features, int depth, int batch, int parts, bool grad) {
   const int slots = (depth + kSlotDepth - 1) / kSlotDepth;
-  const int most = parts > 1 ? 128 : 256;
-  const int t_tiles = (batch + most - 1) / most;
-  int nt = ((batch + t_tiles - 1) / t_tiles + 15) / 16 * 16;
   const int f_tiles = (features + kF - 1) / kF;
-  if (batch > 128 && static_cast<long long>(f_tiles + 1) / 2 * t_tiles >= kSms / 4) return {(nt + 31) / 32 * 32, 2, 1};
+  const auto even = [&](int most, int unit) {
+    const int t_tiles = (batch + most - 1) / most;
+    return ((batch + t_tiles - 1) / t_tiles + unit - 1) / unit * unit;
+  };
+  if (batch > 128) {
+    const int nt = even(256 / parts, 32);
+    if (static_cast<long long>(f_tiles + 1) / 2 * ((batch + nt - 1) / nt) >= kSms / 4) return {nt, 2, 1};
+  }
+  const int nt = even((grad ? 192 : 128) / parts, 16);
+  const int t_tiles = (batch + nt - 1) / nt;
   int splits = 1;
-  while (splits < 8 && static_cast<long long>(f_tiles) * t_tiles * splits * 2 <= kSms && slots >= 2 * splits * 2 && nt <= 128)
+  while (splits < 8 && static_cast<long long>(f_tiles) * t_tiles * splits * 2 <= kSms && slots >= 2 * splits * 2)
     splits *= 2;
   return {nt, 1, splits};
 }
@@ -575,7 +575,7 @@ cudaError_t launch_linear(const Call& c, const Tiling& tl, uint32_t* status, cud
   }
   CUtensorMap x_map, w_map;
   e = map_2d(&x_map, TYPE == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, c.depth,
-             static_cast<uint64_t>(c.batch) * parts, static_cast<uint64_t>(pitch) * 2, kDepth, tl.nt / CG,
+             static_cast<uint64_t>(c.batch) * parts, static_cast<uint64_t>(pitch) * 2, 64, tl.nt / CG,
              CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   e = map_2d(&w_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.w.packed, c.K / 2, c.w.rows, c.K / 2, GRAD ? 64 : 128,
@@ -596,8 +596,6 @@ cudaError_t launch_linear(const Call& c, const Tiling& tl, uint32_t* status, cud
   q.t_tiles = (c.batch + tl.nt - 1) / tl.nt;
   q.splits = tl.splits;
   q.parts = parts;
-  const int stage = tl.nt / CG * 128 * parts;
-  q.x_stages = S::kXBytes / stage < kDone ? S::kXBytes / stage : kDone;
   q.out_type = c.type;
   const long long tiles = static_cast<long long>(q.f_tiles) * q.t_tiles;
   if (tiles > 0x7FFFFFFF / 8) return cudaErrorInvalidValue;
@@ -611,7 +609,7 @@ cudaError_t launch_linear(const Call& c, const Tiling& tl, uint32_t* status, cud
 
 template <bool GRAD>
 cudaError_t run(const Call& c, uint32_t* status, cudaStream_t stream) {
-  const Tiling tl = plan(c.features, c.depth, c.batch, split_parts(c.type, c.format) ? 2 : 1);
+  const Tiling tl = plan(c.features, c.depth, c.batch, split_parts(c.type, c.format) ? 2 : 1, GRAD);
 #define MX4_CASE(f, t) \
   return tl.cg == 2 ? launch_linear<f, t, GRAD, 2>(c, tl, status, stream) : launch_linear<f, t, GRAD, 1>(c, tl, status, stream);
   if (c.format == kMxfp4) { MX4_CASE(kMxfp4, kBf16) }

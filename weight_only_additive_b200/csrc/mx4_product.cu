@@ -59,10 +59,13 @@ struct ProductParams {
   int m_tiles, n_tiles, splits, y_type;
 };
 
-__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t smem) {
-  // 32 rows of 16 bytes, 8-row groups 128 bytes apart, no swizzle
-  const uint64_t desc = static_cast<uint64_t>((smem >> 4) & 0x3FFFu) | static_cast<uint64_t>(128u >> 4) << 32 |
-                        static_cast<uint64_t>(1u) << 46;
+// Shared-memory descriptor of a 512-byte scale tile: 32 rows of 16 bytes, 8-row groups 128
+// bytes apart, no swizzle.
+__device__ __forceinline__ uint64_t scales_desc(uint32_t smem) {
+  return static_cast<uint64_t>((smem >> 4) & 0x3FFFu) | static_cast<uint64_t>(128u >> 4) << 32 |
+         static_cast<uint64_t>(1u) << 46;
+}
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t failed;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     failed = 0;
     for (int i = 0; i < P::kStages; ++i) {
@@ -174,10 +177,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   const int s0 = k_stages * rank / p.splits, s1 = k_stages * (rank + 1) / p.splits;
   const int total = p.m_tiles * p.n_tiles;
   const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
-  // a wait that gives up makes every later one in this CTA end at once
+  // a wait that gives up makes every later one of this CTA that is not over end soon
   const auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-    if (failed) return false;
-    if (mbar_wait_bounded(bar, parity, p.status, site)) return true;
+    if (mbar_wait_sleeping<false>(bar, parity, p.status, site, &failed)) return true;
     failed = 1;
     return false;
   };
@@ -185,80 +187,88 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   if (warp == 0 && lane == 0) {
     // ---- loads
     const uint64_t keep = l2_policy_evict_last(), pass = l2_policy_evict_first();
-    const int x_row_tiles = (p.batch + 127) / 128, w_row_tiles = (p.N + 127) / 128;
-    uint32_t it = 0, landed = 0;
+    const int w_row_tiles = (p.N + 127) / 128;
+    Ring<P::kStages> r;
+    uint32_t issued = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
       const int m = t % p.m_tiles, n0 = (t / p.m_tiles) * NT;
-      for (int s = s0; s < s1 && ok; ++s, ++it) {
-        const int slot = it % P::kStages;
-        ok = wait(&empty[slot], ((it / P::kStages) & 1) ^ 1, kSitePipeEmpty);
+      for (int s = s0; s < s1; ++s, r.next(), ++issued) {
+        ok = wait(&empty[r.slot], r.phase ^ 1, kSitePipeEmpty);
         if (!ok) break;
-        const uint32_t base = smem_addr(stages + slot * P::kStage);
+        uint64_t* bar = &full[r.slot];
+        const uint32_t base = smem_addr(stages + r.slot * P::kStage);
         const int c0 = s * P::kTilesK;
         const uint32_t run = static_cast<uint32_t>(min(P::kTilesK, p.tiles - c0)) * 512;
         const int wt = n0 / 128;
         const int w_tiles = min(P::kTilesN, w_row_tiles - wt);
-        mbar_arrive_expect_tx(&full[slot], P::kA + P::kB + run * (1 + w_tiles));
-        tma_load_2d(base, &x_map, s * kRowBytes, m * kRows, &full[slot], keep);
-        tma_load_2d(base + P::kA, &w_map, s * kRowBytes, n0, &full[slot], p.m_tiles > 1 ? keep : pass);
+        mbar_arrive_expect_tx(bar, P::kA + P::kB + run * (1 + w_tiles));
+        tma_load_2d(base, &x_map, s * kRowBytes, m * kRows, bar, keep);
+        tma_load_2d(base + P::kA, &w_map, s * kRowBytes, n0, bar, p.m_tiles > 1 ? keep : pass);
         const uint32_t sa = base + P::kA + P::kB, sb = sa + P::kSa;
-        bulk_load(sa, p.xs + (static_cast<size_t>(m) * p.tiles + c0) * 512, run, &full[slot]);
+        bulk_load(sa, p.xs + (static_cast<size_t>(m) * p.tiles + c0) * 512, run, bar);
         for (int j = 0; j < w_tiles; ++j)
-          bulk_load(sb + j * P::kSa, p.ws + (static_cast<size_t>(wt + j) * p.tiles + c0) * 512, run, &full[slot]);
-        landed = it + 1;
+          bulk_load(sb + j * P::kSa, p.ws + (static_cast<size_t>(wt + j) * p.tiles + c0) * 512, run, bar);
       }
     }
-    (void)x_row_tiles;
-    // copies still in flight after a failure land before the shared memory goes away
-    if (!ok)
-      for (uint32_t j = landed > P::kStages ? landed - P::kStages : 0; j < landed; ++j)
-        mbar_wait_bounded(&full[j % P::kStages], (j / P::kStages) & 1, p.status, kSitePipeFull);
-  } else if (warp == 1 && lane == 0) {
-    // ---- scale copies and MMAs
-    uint32_t it = 0, acc_it = 0;
+    // after a failure what was asked for lands before the shared memory goes away
+    if (!ok && issued) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 1000000) {
+      }
+    }
+  } else if (warp == 1) {
+    // ---- scale copies and MMAs: the whole warp walks the stages, so that descriptors stay
+    // in uniform registers; one lane issues
+    const bool issuer = elect_one();
+    const uint64_t a_desc = umma_desc_sw128_kmajor(smem_addr(stages)), s_desc = scales_desc(smem_addr(stages) + P::kA + P::kB);
+    Ring<P::kStages> r;
+    Ring<P::kScaleBufs> sc;
+    uint32_t acc_it = 0, it = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step, ++acc_it) {
       const int n0 = (t / p.m_tiles) * NT;
       const uint32_t shift = (n0 & 127) / 32;  // the tile's first scale column
-      const int acc = acc_it % P::kAccs;
+      const uint32_t acc = acc_it % P::kAccs;
       ok = wait(&acc_empty[acc], ((acc_it / P::kAccs) & 1) ^ 1, kSitePipeAcc);
       tc_fence_after_sync();
       const uint32_t d = tmem + acc * NT;
-      for (int s = s0; s < s1 && ok; ++s, ++it) {
-        const int slot = it % P::kStages;
-        ok = wait(&full[slot], (it / P::kStages) & 1, kSitePipeFull);
+      uint32_t go = 0;
+      for (int s = s0; s < s1 && ok; ++s, r.next(), sc.next(), ++it) {
+        ok = wait(&full[r.slot], r.phase, kSitePipeFull);
         // the scale columns' last readers: the MMAs kScaleBufs stages ago
-        if (ok && P::kScaleBufs < P::kStages && it >= P::kScaleBufs) {
+        if (P::kScaleBufs < P::kStages && ok && it >= P::kScaleBufs) {
           const uint32_t old = it - P::kScaleBufs;
           ok = wait(&empty[old % P::kStages], (old / P::kStages) & 1, kSitePipeEmpty);
         }
         if (!ok) break;
         tc_fence_after_sync();
-        const uint32_t base = smem_addr(stages + slot * P::kStage);
-        const uint32_t sa = base + P::kA + P::kB, sb = sa + P::kSa;
-        const uint32_t ta = scale_tmem + (it % P::kScaleBufs) * P::kScaleCols, tb = ta + P::kTilesK * 4;
-        const int steps = min(kStageK / kStepK, (p.K - s * kStageK + kStepK - 1) / kStepK);
+        const uint64_t da = a_desc + r.slot * (P::kStage >> 4), db = da + (P::kA >> 4);
+        const uint64_t sa = s_desc + r.slot * (P::kStage >> 4), sb = sa + (P::kSa >> 4);
+        const uint32_t ta = scale_tmem + sc.slot * P::kScaleCols, tb = ta + P::kTilesK * 4;
+        const int steps = (p.K - s * kStageK + kStepK - 1) / kStepK;
+        if (issuer) {
 #pragma unroll
-        for (int c = 0; c < P::kTilesK; ++c) {
-          tmem_copy_scales(ta + c * 4, sa + c * 512);
+          for (int c = 0; c < P::kTilesK; ++c) {
+            tmem_copy_scales(ta + c * 4, sa + c * (512 >> 4));
 #pragma unroll
-          for (int j = 0; j < P::kTilesN; ++j)
-            tmem_copy_scales(tb + (c * P::kTilesN + j) * 4, sb + j * P::kSa + c * 512);
+            for (int j = 0; j < P::kTilesN; ++j)
+              tmem_copy_scales(tb + (c * P::kTilesN + j) * 4, sb + (j * P::kSa + c * 512) / 16);
+          }
+#pragma unroll
+          for (int k = 0; k < kStageK / kStepK; ++k) {
+            // 64 values: two MXFP4 scales of a word, or all four NVFP4 scales of one
+            const int c = FORMAT == kMxfp4 ? k / 2 : k;
+            const uint32_t sf = FORMAT == kMxfp4 ? (k & 1) * 2 : 0;
+            if (k < steps)
+              umma_mx4<FORMAT>(d, da + k * 2, db + k * 2, mx4_idesc<FORMAT>(NT, sf), ta + c * 4,
+                               tb + c * P::kTilesN * 4 + shift, k > 0 ? 1 : go);
+          }
+          umma_commit(&empty[r.slot]);
         }
-        const uint64_t da = umma_desc_sw128_kmajor(base), db = umma_desc_sw128_kmajor(base + P::kA);
-#pragma unroll
-        for (int k = 0; k < kStageK / kStepK; ++k) {
-          if (k >= steps) break;
-          // 64 values: two MXFP4 scales of a word, or all four NVFP4 scales of one
-          const int c = FORMAT == kMxfp4 ? k / 2 : k;
-          const uint32_t sf = FORMAT == kMxfp4 ? (k & 1) * 2 : 0;
-          umma_mx4<FORMAT>(d, da + k * 2, db + k * 2, mx4_idesc<FORMAT>(NT, sf), ta + c * 4,
-                           tb + c * P::kTilesN * 4 + shift, s > s0 || k > 0);
-        }
-        umma_commit(&empty[slot]);
+        go = 1;
       }
-      if (ok) umma_commit(&acc_full[acc]);
+      if (ok && issuer) umma_commit(&acc_full[acc]);
     }
   } else if (warp >= 2) {
     // ---- results
@@ -271,8 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (int t = first; t < total && ok; t += step, ++acc_it) {
       const int m0 = (t % p.m_tiles) * kRows, n0 = (t / p.m_tiles) * NT;
       const int acc = acc_it % P::kAccs;
-      ok = wait(&acc_full[acc], (acc_it / P::kAccs) & 1, kSitePipeAcc);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      // one lane waits for its warp
+      ok = __shfl_sync(0xFFFFFFFFu, lane == 0 ? wait(&acc_full[acc], (acc_it / P::kAccs) & 1, kSitePipeAcc) : false, 0);
+      if (!ok) break;
       tc_fence_after_sync();
       const int row = m0 + quad * 32 + lane;
       const uint32_t lane_base = tmem + acc * NT + (static_cast<uint32_t>(quad * 32) << 16);

@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* __r
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         uint32_t pairs[4];
-        e2m1x8_to_f16(words[2 * h + j], pairs);
+        e2m1x8_decode<kF16>(words[2 * h + j], pairs);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 q = h2_to_f2(pairs[i]);
