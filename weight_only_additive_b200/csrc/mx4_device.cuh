@@ -169,11 +169,14 @@ struct Ring {
   }
 };
 
-// Arrive on the same barrier of the cluster's CTA 0.
+// Arrive on the same barrier of the cluster's CTA 0, after this thread's shared-memory
+// accesses and those it has waited for.  The fence is restricted to shared memory: a release
+// of global memory too took about 1000 cycles a stage (2048 x 4096 x 11008: 172 -> 136 us).
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar)) : "memory");
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // tcgen05 instructions of one CTA (CG 1) or of a pair (CG 2: the even CTA issues for both;
