@@ -209,6 +209,29 @@ __device__ __forceinline__ void umma_commit_cg(uint64_t* bar) {
   }
 }
 
+// Load 32 consecutive 32-bit columns of this warp's 32 TMEM lanes; the values are there
+// after tmem_ld_wait().
+__device__ __forceinline__ void tmem_ld_x32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[N][32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  // the values are used after the wait, not between
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(v[i][j]));
+}
+
 // Launch with programmatic stream serialisation: the kernel's start overlaps the end of
 // the one before it, and its grid_dependency_wait() orders its memory accesses after it.
 template <typename... Params, typename... Args>

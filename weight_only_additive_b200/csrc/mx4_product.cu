@@ -2,7 +2,9 @@
 // tensor-core path (tcgen05.mma kind::mxf4 / kind::mxf4nvf4): the scales are applied
 // inside the MMA, sums are fp32.
 //
-// A CTA computes 128 tokens x NT features.  A stage is 256 values of K: 128-byte packed
+// A CTA computes 128 tokens x NT features; with many tokens a pair of CTAs (cta_group::2)
+// computes 256 x 256, each loading half of the weights' rows, since the traffic from L2
+// bounds a single CTA's tile.  A stage is 256 values of K: 128-byte packed
 // rows of both operands by TMA (128-byte swizzle) and their scales as whole 512-byte
 // tiles, which tcgen05.cp spreads over the four TMEM lane quadrants as the MMA wants
 // them.  One thread loads, one issues copies and MMAs, eight warps write results.
@@ -20,17 +22,16 @@ constexpr int kStageK = 256;         // values of K in a stage
 constexpr int kRowBytes = kStageK / 2;
 constexpr int kStepK = 64;           // values of K in one MMA
 constexpr int kThreads = 320;        // load warp, MMA warp, 8 epilogue warps
-constexpr int kEpilogue = 256;
 constexpr int kMaxSmem = 227 * 1024;
 
 constexpr int round_pow2(int v) { return v <= 32 ? 32 : v <= 64 ? 64 : v <= 128 ? 128 : v <= 256 ? 256 : 512; }
 
 // Shapes that follow from the format and the tile width.
-template <int FORMAT, int NT>
+template <int FORMAT, int NT, int CG>
 struct Plan {
   static constexpr int kTilesK = kStageK / (4 * mx4_block(FORMAT));  // scale tiles of a stage along K
   static constexpr int kTilesN = NT > 128 ? 2 : 1;                   // and along the features
-  static constexpr int kA = kRows * kRowBytes, kB = NT * kRowBytes;
+  static constexpr int kA = kRows * kRowBytes, kB = NT / CG * kRowBytes;
   static constexpr int kSa = kTilesK * 512, kSb = kTilesN * kTilesK * 512;
   static constexpr int kStage = kA + kB + ((kSa + kSb + 1023) & ~1023);
   static constexpr int kFit = (kMaxSmem - 2048) / kStage;
@@ -42,7 +43,9 @@ struct Plan {
   static constexpr int kScaleBufs = kFitScales > kStages ? kStages : kFitScales;
   static constexpr int kCols = round_pow2(kAccs * NT + kScaleBufs * kScaleCols);
   static constexpr int kRedPitch = NT + 4;  // floats of a partial row: 16-byte stores of 8 lanes hit all banks
+  static_assert(CG == 1 || NT == 256, "a pair's halves are whole scale tiles");
   static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStage + 2048;
+  static_assert((NT / 2) % 32 == 0, "a warp's columns");
   static_assert(kStages >= 3 && kScaleBufs >= 2 && kCols <= 512, "");
   static_assert(kRows * kRedPitch * 4 <= kStages * kStage, "");
 };
@@ -65,51 +68,58 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t smem) {
   return static_cast<uint64_t>((smem >> 4) & 0x3FFFu) | static_cast<uint64_t>(128u >> 4) << 32 |
          static_cast<uint64_t>(1u) << 46;
 }
+template <int CG>
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  if constexpr (CG == 1) asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // Instruction descriptor of the block-scaled MMA: e2m1 operands (code 1), both K-major.
 //   bits 4-5 / 29-30 byte of the scale word that B's / A's scales start at
 //   bits 7-9 / 10-12 operand types, 17-22 N >> 3, 23 scale type (1: e8m0), 24-28 M >> 4
-template <int FORMAT>
+template <int FORMAT, int CG>
 __host__ __device__ constexpr uint32_t mx4_idesc(uint32_t n, uint32_t sf) {
-  return sf << 4 | 1u << 7 | 1u << 10 | (n >> 3) << 17 | (FORMAT == kMxfp4 ? 1u : 0u) << 23 | (kRows >> 4) << 24 |
+  return sf << 4 | 1u << 7 | 1u << 10 | (n >> 3) << 17 | (FORMAT == kMxfp4 ? 1u : 0u) << 23 | (kRows * CG >> 4) << 24 |
          sf << 29;
 }
 
-template <int FORMAT>
+template <int FORMAT, int CG>
 __device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
                                          uint32_t accumulate) {
-  if constexpr (FORMAT == kMxfp4) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate) : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate) : "memory");
-  }
+#define MX4_MMA(group, kind)                                                                       \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                  \
+               "tcgen05.mma.cta_group::" group "." kind " [%0], %1, %2, %3, [%4], [%5], p;\n\t}"    \
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate) : "memory")
+  if constexpr (FORMAT == kMxfp4 && CG == 1) MX4_MMA("1", "kind::mxf4.block_scale.scale_vec::2X");
+  else if constexpr (FORMAT == kMxfp4) MX4_MMA("2", "kind::mxf4.block_scale.scale_vec::2X");
+  else if constexpr (CG == 1) MX4_MMA("1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+  else MX4_MMA("2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+#undef MX4_MMA
 }
 
-// bias[c .. c + 8) as fp32 (zeros without one; c + 8 <= N)
+// bias[c .. c + 8) as fp32; `c` in whole 16-byte units
 __device__ __forceinline__ void bias8(const void* bias, int type, size_t c, float (&b)[8]) {
+  if (type == kF32) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(bias) + c);
+    const float4 u = q[0], v = q[1];
+    b[0] = u.x, b[1] = u.y, b[2] = u.z, b[3] = u.w, b[4] = v.x, b[5] = v.y, b[6] = v.z, b[7] = v.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(bias) + c);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    b[i] = !bias ? 0.0f
-           : type == kF16  ? load_value<kF16>(bias, c + i)
-           : type == kBf16 ? load_value<kBf16>(bias, c + i)
-                           : load_value<kF32>(bias, c + i);
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = type == kF16 ? h2_to_f2(w[i]) : b2_to_f2(w[i]);
+      b[2 * i] = f.x, b[2 * i + 1] = f.y;
+    }
+  }
 }
 
 // v[0..8) * scale + bias to y[row][c ..); `vec`: rows of y are whole 16-byte units.
 __device__ __forceinline__ void put8(const ProductParams& p, int row, int c, const float* v, float scale, bool vec) {
   const size_t at = static_cast<size_t>(row) * p.N + c;
   if (vec && c + 8 <= p.N) {
-    float b[8], o[8];
-    bias8(p.bias, p.y_type, c, b);
+    float b[8] = {}, o[8];
+    if (p.bias) bias8(p.bias, p.y_type, c, b);
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = fmaf(v[i], scale, b[i]);
     if (p.y_type == kF32) {
@@ -138,11 +148,11 @@ __device__ __forceinline__ void put8(const ProductParams& p, int row, int c, con
   }
 }
 
-template <int FORMAT, int NT>
+template <int FORMAT, int NT, int CG>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ CUtensorMap x_map,
                                                               const __grid_constant__ CUtensorMap w_map,
                                                               const ProductParams p) {
-  using P = Plan<FORMAT, NT>;
+  using P = Plan<FORMAT, NT, CG>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[P::kStages], empty[P::kStages], acc_full[P::kAccs], acc_empty[P::kAccs];
@@ -150,21 +160,23 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   __shared__ volatile uint32_t failed;
 
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
+  const int rank = CG > 1 || p.splits > 1 ? static_cast<int>(cluster_rank()) : 0;
   if (threadIdx.x == 0) {
     failed = 0;
     for (int i = 0; i < P::kStages; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], CG > 1 && rank == 0 ? 2 : 1);  // a pair's first CTA also waits for its second
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < P::kAccs; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], kEpilogue);
+      mbar_init(&acc_empty[i], 8 * CG);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tmem_alloc(&tmem_slot, P::kCols);
+  if (warp == 1) tmem_alloc_cg<CG>(&tmem_slot, P::kCols);
   tc_fence_before_sync();
   __syncthreads();
+  if (CG > 1) cluster_sync();  // the pair's barriers are ready before either arrives on them
   tc_fence_after_sync();
   const uint32_t tmem = tmem_slot;
   const uint32_t scale_tmem = tmem + P::kAccs * NT;
@@ -173,13 +185,19 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   grid_dependents_launch();
 
   const int k_stages = (p.K + kStageK - 1) / kStageK;
-  const int rank = p.splits > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int s0 = k_stages * rank / p.splits, s1 = k_stages * (rank + 1) / p.splits;
+  const int k_rank = CG > 1 ? 0 : rank, pair_rank = CG > 1 ? rank : 0;
+  const int s0 = k_stages * k_rank / p.splits, s1 = k_stages * (k_rank + 1) / p.splits;
   const int total = p.m_tiles * p.n_tiles;
-  const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
+  const int per = CG > 1 ? CG : p.splits;
+  const int first = blockIdx.x / per, step = gridDim.x / per;
   // a wait that gives up makes every later one of this CTA that is not over end soon
   const auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
     if (mbar_wait_sleeping<false>(bar, parity, p.status, site, &failed)) return true;
+    failed = 1;
+    return false;
+  };
+  const auto wait_pair = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+    if (mbar_wait_sleeping<(CG > 1)>(bar, parity, p.status, site, &failed)) return true;
     failed = 1;
     return false;
   };
@@ -187,12 +205,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   if (warp == 0 && lane == 0) {
     // ---- loads
     const uint64_t keep = l2_policy_evict_last(), pass = l2_policy_evict_first();
-    const int w_row_tiles = (p.N + 127) / 128;
+    const int w_row_tiles = (p.N + 127) / 128, x_row_tiles = (p.batch + 127) / 128;
     Ring<P::kStages> r;
     uint32_t issued = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
-      const int m = t % p.m_tiles, n0 = (t / p.m_tiles) * NT;
+      const int m = (t % p.m_tiles) * CG + pair_rank, n0 = (t / p.m_tiles) * NT;
       for (int s = s0; s < s1; ++s, r.next(), ++issued) {
         ok = wait(&empty[r.slot], r.phase ^ 1, kSitePipeEmpty);
         if (!ok) break;
@@ -202,11 +220,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const uint32_t run = static_cast<uint32_t>(min(P::kTilesK, p.tiles - c0)) * 512;
         const int wt = n0 / 128;
         const int w_tiles = min(P::kTilesN, w_row_tiles - wt);
-        mbar_arrive_expect_tx(bar, P::kA + P::kB + run * (1 + w_tiles));
+        const int x_tiles = m < x_row_tiles;  // a pair's second CTA may have no tokens: it reads zeros
+        mbar_arrive_expect_tx(bar, P::kA + P::kB + run * (x_tiles + w_tiles));
         tma_load_2d(base, &x_map, s * kRowBytes, m * kRows, bar, keep);
-        tma_load_2d(base + P::kA, &w_map, s * kRowBytes, n0, bar, p.m_tiles > 1 ? keep : pass);
+        tma_load_2d(base + P::kA, &w_map, s * kRowBytes, n0 + pair_rank * (NT / CG), bar, p.m_tiles > 1 ? keep : pass);
         const uint32_t sa = base + P::kA + P::kB, sb = sa + P::kSa;
-        bulk_load(sa, p.xs + (static_cast<size_t>(m) * p.tiles + c0) * 512, run, bar);
+        if (x_tiles) bulk_load(sa, p.xs + (static_cast<size_t>(m) * p.tiles + c0) * 512, run, bar);
         for (int j = 0; j < w_tiles; ++j)
           bulk_load(sb + j * P::kSa, p.ws + (static_cast<size_t>(wt + j) * p.tiles + c0) * 512, run, bar);
       }
@@ -217,6 +236,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       while (global_timer_ns() - t0 < 1000000) {
       }
     }
+  } else if (warp == 1 && CG > 1 && rank > 0) {
+    // ---- the pair's second CTA tells the first when its part of a stage is there
+    Ring<P::kStages> r;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step)
+      for (int s = s0; s < s1 && ok; ++s, r.next()) {
+        ok = __shfl_sync(0xFFFFFFFFu, lane == 0 ? wait(&full[r.slot], r.phase, kSitePipeFull) : false, 0);
+        if (ok && lane == 0) mbar_arrive_leader(&full[r.slot]);
+      }
   } else if (warp == 1) {
     // ---- scale copies and MMAs: the whole warp walks the stages, so that descriptors stay
     // in uniform registers; one lane issues
@@ -230,12 +258,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const int n0 = (t / p.m_tiles) * NT;
       const uint32_t shift = (n0 & 127) / 32;  // the tile's first scale column
       const uint32_t acc = acc_it % P::kAccs;
-      ok = wait(&acc_empty[acc], ((acc_it / P::kAccs) & 1) ^ 1, kSitePipeAcc);
+      ok = wait_pair(&acc_empty[acc], ((acc_it / P::kAccs) & 1) ^ 1, kSitePipeAcc);
       tc_fence_after_sync();
       const uint32_t d = tmem + acc * NT;
       uint32_t go = 0;
       for (int s = s0; s < s1 && ok; ++s, r.next(), sc.next(), ++it) {
-        ok = wait(&full[r.slot], r.phase, kSitePipeFull);
+        ok = wait_pair(&full[r.slot], r.phase, kSitePipeFull);
         // the scale columns' last readers: the MMAs kScaleBufs stages ago
         if (P::kScaleBufs < P::kStages && ok && it >= P::kScaleBufs) {
           const uint32_t old = it - P::kScaleBufs;
@@ -250,10 +278,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         if (issuer) {
 #pragma unroll
           for (int c = 0; c < P::kTilesK; ++c) {
-            tmem_copy_scales(ta + c * 4, sa + c * (512 >> 4));
+            tmem_copy_scales<CG>(ta + c * 4, sa + c * (512 >> 4));
 #pragma unroll
             for (int j = 0; j < P::kTilesN; ++j)
-              tmem_copy_scales(tb + (c * P::kTilesN + j) * 4, sb + (j * P::kSa + c * 512) / 16);
+              tmem_copy_scales<CG>(tb + (c * P::kTilesN + j) * 4, sb + (j * P::kSa + c * 512) / 16);
           }
 #pragma unroll
           for (int k = 0; k < kStageK / kStepK; ++k) {
@@ -261,14 +289,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int c = FORMAT == kMxfp4 ? k / 2 : k;
             const uint32_t sf = FORMAT == kMxfp4 ? (k & 1) * 2 : 0;
             if (k < steps)
-              umma_mx4<FORMAT>(d, da + k * 2, db + k * 2, mx4_idesc<FORMAT>(NT, sf), ta + c * 4,
+              umma_mx4<FORMAT, CG>(d, da + k * 2, db + k * 2, mx4_idesc<FORMAT, CG>(NT, sf), ta + c * 4,
                                tb + c * P::kTilesN * 4 + shift, k > 0 ? 1 : go);
           }
-          umma_commit(&empty[r.slot]);
+          umma_commit_cg<CG>(&empty[r.slot]);
         }
         go = 1;
       }
-      if (ok && issuer) umma_commit(&acc_full[acc]);
+      if (ok && issuer) umma_commit_cg<CG>(&acc_full[acc]);
     }
   } else if (warp >= 2) {
     // ---- results
@@ -279,31 +307,40 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     uint32_t acc_it = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step, ++acc_it) {
-      const int m0 = (t % p.m_tiles) * kRows, n0 = (t / p.m_tiles) * NT;
-      const int acc = acc_it % P::kAccs;
+      const int m0 = ((t % p.m_tiles) * CG + pair_rank) * kRows, n0 = (t / p.m_tiles) * NT;
+      const uint32_t acc = acc_it % P::kAccs;
       // one lane waits for its warp
       ok = __shfl_sync(0xFFFFFFFFu, lane == 0 ? wait(&acc_full[acc], (acc_it / P::kAccs) & 1, kSitePipeAcc) : false, 0);
       if (!ok) break;
       tc_fence_after_sync();
       const int row = m0 + quad * 32 + lane;
       const uint32_t lane_base = tmem + acc * NT + (static_cast<uint32_t>(quad * 32) << 16);
-#pragma unroll 1
-      for (int c = half * (NT / 2); c < (half + 1) * (NT / 2); c += 32) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(lane_base + c, v);
-        const float* f = reinterpret_cast<const float*>(v);
+      // the warp's columns into registers at once, so that the next tile's MMAs can begin
+      constexpr int kMine = NT / 2, kParts = (kMine + 31) / 32;
+      uint32_t v[kParts][32];
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) tmem_ld_x32_start(lane_base + half * kMine + i * 32, v[i]);
+      tmem_ld_wait(v);
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 1) mbar_arrive(&acc_empty[acc]);
+        else mbar_arrive_leader(&acc_empty[acc]);
+      }
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) {
+        const int c = half * kMine + i * 32;
+        const float* f = reinterpret_cast<const float*>(v[i]);
         if (p.splits > 1) {
           float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(stages) + (quad * 32 + lane) * P::kRedPitch + c);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) q[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+          for (int e = 0; e < 8; ++e) q[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
         } else if (row < p.batch) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (n0 + c + 8 * i < p.N) put8(p, row, n0 + c + 8 * i, f + 8 * i, scale, vec);
+          for (int e = 0; e < 4; ++e)
+            if (n0 + c + 8 * e < p.N) put8(p, row, n0 + c + 8 * e, f + 8 * e, scale, vec);
         }
       }
-      tc_fence_before_sync();
-      mbar_arrive(&acc_empty[acc]);
     }
   }
 
@@ -332,8 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     cluster_sync();  // no CTA leaves while another reads its partial tile
   }
   tc_fence_before_sync();
+  __syncwarp();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, P::kCols);
+  if (CG > 1) cluster_sync();
+  if (warp == 1) tmem_dealloc_cg<CG>(tmem, P::kCols);
 }
 
 // Packed rows as a 2-D map of bytes: boxes of 128 bytes x `box` rows, 128-byte swizzle.
@@ -353,12 +392,12 @@ cudaError_t packed_map(CUtensorMap* map, const Mx4& t, int K, int box) {
 
 constexpr int kSms = 148;
 
-template <int FORMAT, int NT>
+template <int FORMAT, int NT, int CG = 1>
 cudaError_t product_as(const Mx4Product& p, int splits, uint32_t* status, cudaStream_t stream) {
-  using P = Plan<FORMAT, NT>;
+  using P = Plan<FORMAT, NT, CG>;
   CUtensorMap x_map, w_map;
   cudaError_t e = packed_map(&x_map, p.x, p.K, kRows);
-  if (e == cudaSuccess) e = packed_map(&w_map, p.w, p.K, NT);
+  if (e == cudaSuccess) e = packed_map(&w_map, p.w, p.K, NT / CG);
   if (e != cudaSuccess) return e;
   ProductParams q{};
   q.xs = p.x.scales;
@@ -372,17 +411,18 @@ cudaError_t product_as(const Mx4Product& p, int splits, uint32_t* status, cudaSt
   q.N = p.w.rows;
   q.K = p.K;
   q.tiles = mx4_scale_tiles(p.K, FORMAT);
-  q.m_tiles = (q.batch + kRows - 1) / kRows;
+  q.m_tiles = (q.batch + kRows * CG - 1) / (kRows * CG);
   q.n_tiles = (q.N + NT - 1) / NT;
   q.splits = splits;
   q.y_type = p.y_type;
-  auto* kernel = product_kernel<FORMAT, NT>;
+  auto* kernel = product_kernel<FORMAT, NT, CG>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(P::kSmem));
   if (e != cudaSuccess) return e;
   const long long tiles = static_cast<long long>(q.m_tiles) * q.n_tiles;
-  if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const unsigned grid = splits > 1 ? static_cast<unsigned>(tiles * splits) : static_cast<unsigned>(tiles < kSms ? tiles : kSms);
-  return launch_overlapped(kernel, grid, kThreads, P::kSmem, stream, splits, x_map, w_map, q);
+  if (tiles > 0x7FFFFFFF / 8) return cudaErrorInvalidValue;
+  const long long ctas = tiles * CG * splits;
+  const unsigned grid = static_cast<unsigned>(splits > 1 || ctas < kSms ? ctas : kSms);
+  return launch_overlapped(kernel, grid, kThreads, P::kSmem, stream, CG * splits, x_map, w_map, q);
 }
 
 // Tile width and K split.  A tile's time is its MMAs (2 cycles per feature and 64 values
@@ -405,6 +445,8 @@ cudaError_t product_planned(const Mx4Product& p, uint32_t* status, cudaStream_t 
       if (cost < best) best = cost, best_nt = nt, best_split = split;
     }
   }
+  const long long pairs = (m_tiles + 1) / 2 * ((p.w.rows + 255) / 256);
+  if (m_tiles > 1 && pairs >= kSms / 4) return product_as<FORMAT, 256, 2>(p, 1, status, stream);
   switch (best_nt) {
     case 64: return product_as<FORMAT, 64>(p, best_split, status, stream);
     case 128: return product_as<FORMAT, 128>(p, best_split, status, stream);
