@@ -621,13 +621,14 @@ cudaError_t run(const Call& c, uint32_t* status, cudaStream_t stream) {
 }  // namespace
 
 size_t mx4_linear_workspace(int type, int format, long long K, long long batch) {
-  return restaged_bytes(type, format, K, batch);
+  return batch <= 0x7FFFFFFF && mx4_gemv_takes(static_cast<int>(batch)) ? 0 : restaged_bytes(type, format, K, batch);
 }
 size_t mx4_grad_workspace(int type, int format, long long N, long long batch) {
   return restaged_bytes(type, format, N, batch);
 }
 
 cudaError_t launch_mx4_linear(const Mx4Linear& p, uint32_t* status, cudaStream_t stream) {
+  if (mx4_gemv_takes(p.batch)) return launch_mx4_gemv(p, stream);
   return run<false>(Call{p.x, p.w, p.bias, p.y, p.type, p.w.rows, p.K, p.K, p.batch, p.format, p.workspace}, status, stream);
 }
 
