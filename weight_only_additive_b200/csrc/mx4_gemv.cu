@@ -1,38 +1,57 @@
 // y = x . W^T + bias with 16-bit x and microscaled 4-bit W, for a few tokens: bound by
-// reading the weights, so they go from global memory to registers, are decoded there and
-// multiplied by mma.sync (16 rows x 8 tokens x 16 values), which keeps the arithmetic per
-// weight well below what fp32 FMAs would take.
+// reading the weights.  They are decoded in registers and multiplied by mma.sync (16 rows x
+// 8 tokens x 16 values), which keeps the arithmetic per weight well below fp32 FMAs.
 //
-// A warp has 32 weight rows, eight neighbours in each of the four 32-row parts of a scale
-// tile, so that one 16-byte load brings the four rows' scales of four blocks.  In a step of
-// 128 values lane (g, t) reads 32 of them (16 bytes) in rows g of the four parts.  Which of
-// the 128 values an MMA takes is free as long as x is taken alike: a word's nibbles j and
-// j + 4 make a pair, which costs two shifts and two logic operations to form.
+// Persistent CTAs, one an SM, walk units of 32 weight rows.  A stage is 1024 values of them:
+// four 128-byte-swizzled TMA boxes and the scale tiles, in a ring that runs across units, so
+// that the reads never pause.  (Loads by the lanes that use the values, 16 bytes of a row
+// each, reached a third of the bandwidth, from registers or by cp.async.)  Two sets of eight
+// warps take stages in turn, a warp 128 values of the 32 rows; lane (g, t) has 32 of them in
+// four rows.  Which of the 128
+// values an MMA takes is free as long as x is taken alike.  The partial sums of a unit are
+// fp32, added in a fixed order; with few units a cluster of CTAs splits the reduction.
 //
-// The decoded weight is exact: bf16 holds e2m1 times 2^e or e4m3, fp16 holds e2m1 * e4m3 *
-// 2^-14 (a multiple of 2^-24).  fp16 x with MXFP4 weights is split into two bf16 parts.
+// Decoding is a table lookup: a byte of two codes gives their pair.  The table has a copy
+// for every lane, each in its own bank, 256 bytes a row, so that one byte permute makes
+// the address and no lookup conflicts.  The decoded weight is exact: e2m1 times 2^e or e4m3
+// fits bf16, e2m1 times e4m3 fits fp16.  fp16 x with MXFP4 weights is split into two bf16
+// parts.
 //
-// Warps of a CTA and CTAs of a cluster share the reduction; partial sums are fp32, added in
-// a fixed order.
+// One token leaves seven of an MMA's eight columns free.  They take the blocks apart: column
+// 2 t + h holds x where lane t has half h of its 32 values and zeros elsewhere, so that the
+// sums come out per 16 values, and the scales multiply four fp32 sums a step instead of
+// every pair of weights.
 #include "mx4_device.cuh"
 
 namespace aqlm {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kStep = 128;
+constexpr int kSet = 8, kWarps = 2 * kSet, kConsumers = kWarps * 32, kThreads = kConsumers + 32;
+constexpr int kRows = 32, kStage = 1024, kBox = 256, kStep = 128;
+constexpr int kStageBytes = kRows * kStage / 2;
+constexpr int kTableBytes = 65536;
 constexpr int kSms = 148;
 
+template <int FORMAT, int NB>
+struct Shape {
+  static constexpr int kTiles = kStage / (4 * mx4_block(FORMAT));  // scale tiles of a stage
+  static constexpr int kSlot = kStageBytes + kTiles * 512;
+  static constexpr int kPart = 2 * kWarps * kRows * (NB ? NB : 1) * 8 * 4;  // two sets of the warps' sums
+  static constexpr int kFit = (227 * 1024 - 1024 - kTableBytes - kPart - 256) / kSlot;
+  static constexpr int kSlots = kFit > 7 ? 7 : kFit;
+  static constexpr size_t kSmem = 1024 + kTableBytes + kPart + kSlots * kSlot;
+  static_assert(kSlots >= 4, "");
+};
+
 struct GemvParams {
-  const uint8_t* packed;
   const uint8_t* scales;
   const float* gamma;
   const void* x;
   const void* bias;
   void* y;
-  int N, K, batch, tiles;
-  int split_warps;   // warps of a CTA that share rows
-  int split_ctas;    // CTAs of a cluster that do
+  uint32_t* status;
+  int N, K, batch, tiles, units;
+  int splits;  // CTAs of a cluster that share a unit
 };
 
 template <int TYPE>
@@ -46,26 +65,16 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Eight codes as the pairs (j, j + 4), j = 0..3, times `scale`.
-//   fp16: the code's three magnitude bits as the low exponent and top mantissa bits are
-//         e2m1 * 2^-14; the scale comes without that factor, which the caller takes out.
-//   bf16: likewise e2m1 * 2^-126; times 2^126, then times the scale.
-template <int TYPE>
-__device__ __forceinline__ void decode_pairs(uint32_t w, uint32_t scale, uint32_t (&h)[4]) {
-  constexpr int kUp = TYPE == kF16 ? 9 : 6;
-  constexpr uint32_t kMask = TYPE == kF16 ? 0x0E000E00u : 0x01C001C0u;
+// Eight codes as four pairs, in order, times `scale` (SCALED); `lane4`: 4 * lane.
+template <int TYPE, bool SCALED>
+__device__ __forceinline__ void decode_pairs(const uint8_t* table, uint32_t lane4, uint32_t w, uint32_t scale,
+                                             uint32_t (&h)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int by = kUp - 4 * j;
-    const uint32_t mag = (by >= 0 ? w << by : w >> -by) & kMask;
-    const uint32_t v = mag | ((w << (12 - 4 * j)) & 0x80008000u);
-    if constexpr (TYPE == kF16) {
-      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[j]) : "r"(v), "r"(scale));
-    } else {
-      uint32_t u;
-      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(u) : "r"(v), "r"(0x7E807E80u));  // 2^126
-      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(h[j]) : "r"(u), "r"(scale));
-    }
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(table + prmt(w, lane4, 0x5504 | j << 4));
+    if constexpr (!SCALED) h[j] = v;
+    else if constexpr (TYPE == kF16) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[j]) : "r"(v), "r"(scale));
+    else asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(h[j]) : "r"(v), "r"(scale));
   }
 }
 
@@ -80,214 +89,313 @@ __device__ __forceinline__ void split_pair(uint32_t x, uint32_t& hi, uint32_t& l
   lo = f2_to_b2_rn(l.x, l.y);
 }
 
-struct Weights {
-  uint4 w[4];  // rows of the four parts
-  uint4 s;     // their scale words
-};
-
+// NB: groups of eight tokens; 0: one token.
 template <int FORMAT, int XT, int NB>
-__global__ void __launch_bounds__(kThreads, NB > 2 ? 1 : 2) gemv_kernel(const GemvParams p) {
-  constexpr bool kSplit = FORMAT == kMxfp4 && XT == kF16;
+__global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant__ CUtensorMap w_map, const GemvParams p) {
+  using S = Shape<FORMAT, NB>;
+  constexpr bool kOne = NB == 0;
+  constexpr int kN = kOne ? 1 : NB;
+  constexpr bool kSplit = !kOne && FORMAT == kMxfp4 && XT == kF16;
   constexpr int TYPE = kSplit ? kBf16 : XT;
-  constexpr int kX = NB * 8;  // tokens
-  __shared__ __align__(16) float part[kWarps * 32 * kX];
+  constexpr int kX = kN * 8;  // columns
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* table = smem_raw + (1024 - (smem_addr(smem_raw) & 1023));
+  float* part = reinterpret_cast<float*>(table + kTableBytes);  // [2][warps][32 rows][columns]
+  const uint32_t ring = smem_addr(table) + kTableBytes + S::kPart;
+  __shared__ uint64_t full[S::kSlots], empty[S::kSlots];
+  __shared__ volatile uint32_t failed;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int rank = p.split_ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int groups = kWarps / p.split_warps;  // 32-row groups of a CTA
-  const int group = (blockIdx.x / p.split_ctas) * groups + warp / p.split_warps;
-  const int tile = group >> 2, row0 = tile * 128 + (group & 3) * 8 + g;  // + 32 q
-  const int first = rank * p.split_warps + warp % p.split_warps, stride = p.split_warps * p.split_ctas;
-  const int steps = (p.K + kStep - 1) / kStep, chunks = p.K / 32;
-
+  const int warp = uniform_warp(), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rank = p.splits > 1 ? static_cast<int>(cluster_rank()) : 0;
+  if (threadIdx.x == 0) {
+    failed = 0;
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kSet);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  const uint32_t lane4 = lane * 4;
+  if (warp < kWarps) {  // the table: each warp's 16 bytes, decoded by a lane each
+    uint32_t h[4];
+    e2m1x8_decode<TYPE>(warp * 16 + (lane & 15), h);
+#pragma unroll
+    for (int b = 0; b < 16; ++b)
+      *reinterpret_cast<uint32_t*>(table + (warp * 16 + b) * 256 + lane4) = __shfl_sync(0xFFFFFFFFu, h[0], b);
+  }
+  __syncthreads();
   grid_dependency_wait();
   grid_dependents_launch();
 
-  const uint64_t stream = l2_policy_evict_first();
-  const uint8_t* rows[4];
-  bool real[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int row = row0 + 32 * q;
-    real[q] = row < p.N;
-    rows[q] = p.packed + static_cast<size_t>(real[q] ? row : 0) * (p.K / 2) + t * 16;
-  }
-  // MXFP4: a step is one scale tile, lane t's block its byte t; NVFP4: two tiles, lane t's
-  // two blocks a half word of tile t / 2
-  const uint8_t* scale_at = p.scales + static_cast<size_t>(tile) * p.tiles * 512 + (row0 & 31) * 16;
-  const auto load = [&](Weights& v, int s) {
-    const bool in = s < steps && s * 4 + t < chunks;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      v.w[q] = in && real[q] ? ldg_stream_v4(rows[q] + static_cast<size_t>(s) * 64, stream) : make_uint4(0, 0, 0, 0);
-    const int c = FORMAT == kMxfp4 ? s : 2 * s + (t >> 1);
-    v.s = in && tile * 128 < p.N ? ldg_nc_v4(scale_at + static_cast<size_t>(c) * 512) : make_uint4(0, 0, 0, 0);
+  const int stages = (p.K + kStage - 1) / kStage, chunks = p.K / 32;
+  const int s0 = stages * rank / p.splits, s1 = stages * (rank + 1) / p.splits;
+  const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
+  const auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+    if (mbar_wait_sleeping<false>(bar, parity, p.status, site, &failed)) return true;
+    failed = 1;
+    return false;
   };
 
-  float acc[2][NB][4] = {};
-  const auto multiply = [&](const Weights& v, int s) {
-    // x, permuted like the weights
-    uint32_t b[NB][16], lo[kSplit ? NB : 1][16];
-    const bool in = s * 4 + t < chunks;
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const int token = n * 8 + g;
-      const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + static_cast<size_t>(token) * p.K +
-                                                       s * kStep + t * 32);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint4 r = make_uint4(0, 0, 0, 0);
-        if (in && token < p.batch) r = ldg_nc_v4(at + i);
-        uint32_t u[4] = {r.x, r.y, r.z, r.w};
-        if constexpr (kSplit) {
-          uint32_t l[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) split_pair(u[k], u[k], l[k]);
-          lo[n][4 * i] = prmt(l[0], l[2], 0x5410), lo[n][4 * i + 1] = prmt(l[0], l[2], 0x7632);
-          lo[n][4 * i + 2] = prmt(l[1], l[3], 0x5410), lo[n][4 * i + 3] = prmt(l[1], l[3], 0x7632);
+  if (warp == kWarps) {
+    // ---- copies
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_first();
+      Ring<S::kSlots> r;
+      bool ok = true;
+      uint32_t issued = 0;
+      for (int u = first; u < p.units && ok; u += step)
+        for (int s = s0; s < s1; ++s, r.next(), ++issued) {
+          ok = wait(&empty[r.slot], r.phase ^ 1, kSitePipeEmpty);
+          if (!ok) break;
+          const uint32_t at = ring + r.slot * S::kSlot;
+          const int boxes = min(kStage / kBox, (p.K - s * kStage + kBox - 1) / kBox);
+          const uint32_t run = static_cast<uint32_t>(min(S::kTiles, p.tiles - s * S::kTiles)) * 512;
+          mbar_arrive_expect_tx(&full[r.slot], boxes * (kRows * kBox / 2) + run);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(at + b * (kRows * kBox / 2), &w_map, s * (kStage / 2) + b * (kBox / 2), u * kRows, &full[r.slot], pol);
+          bulk_load(at + kStageBytes, p.scales + (static_cast<size_t>(u >> 2) * p.tiles + s * S::kTiles) * 512, run,
+                    &full[r.slot]);
         }
-        b[n][4 * i] = prmt(u[0], u[2], 0x5410), b[n][4 * i + 1] = prmt(u[0], u[2], 0x7632);
-        b[n][4 * i + 2] = prmt(u[1], u[3], 0x5410), b[n][4 * i + 3] = prmt(u[1], u[3], 0x7632);
+      if (!ok && issued) {  // what was asked for lands before the shared memory goes away
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000) {
+        }
       }
     }
-    const uint32_t words[4] = {v.s.x, v.s.y, v.s.z, v.s.w};
-    uint32_t scale[4][2];  // of the row's two 16-value halves
+  } else {
+    // ---- products: the 32 rows, values 128 kw .. of a stage.  An MMA's row g is row
+    // g / 2 + 4 (g % 2) of its eight: the eight lanes of a 16-byte read then have two rows
+    // whose swizzled chunks lie in different banks.
+    const int set = warp / kSet, kw = warp % kSet, rr = (g >> 1) | ((g & 1) << 2);
+    const uint32_t from = (kw >> 1) * (kRows * kBox / 2) + rr * 128 + (((((kw & 1) << 2) | t) ^ rr) << 4);
+    // MXFP4: 128 values are one scale tile, the lane's block byte t; NVFP4: two tiles, the
+    // lane's two blocks a half word of tile t / 2
+    const uint32_t from_s = kStageBytes + (FORMAT == kMxfp4 ? kw : 2 * kw + (t >> 1)) * 512 + rr * 16;
+    const float gamma = p.gamma ? *p.gamma : 1.0f;
+    // what a lane holds of x in a step: its 32 values of a token, or half of them or none
+    uint4 x[kN][4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if constexpr (FORMAT == kMxfp4) {
-        const uint32_t e = words[q] >> (8 * t) & 0xFF;
-        scale[q][0] = scale[q][1] = (e == 255 ? 0x7FC0u : max(e << 7, 0x40u)) * 0x10001u;
+    for (int i = 0; i < 4; ++i) x[0][i] = make_uint4(0, 0, 0, 0);
+    const auto load_x = [&](int s) {
+      const int c = s * (kStage / 32) + kw * 4 + t;
+      const uint16_t* from_x = static_cast<const uint16_t*>(p.x) + c * 32;
+      if constexpr (kOne) {
+        const uint4* at = reinterpret_cast<const uint4*>(from_x);
+        if (g >> 1 == t) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i >> 1 == (g & 1)) x[0][i] = c < chunks ? ldg_nc_v4(at + i) : make_uint4(0, 0, 0, 0);
+        }
       } else {
-        uint32_t h;  // two fp16 scales
-        asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(words[q] >> (16 * (t & 1))));
-        if constexpr (TYPE == kBf16) {
-          const float2 f = h2_to_f2(h);
-          h = f2_to_b2_rn(f.x, f.y);
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          const int token = n * 8 + g;
+          const uint4* at = reinterpret_cast<const uint4*>(from_x + static_cast<size_t>(token) * p.K);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[n][i] = c < chunks && token < p.batch ? ldg_nc_v4(at + i) : make_uint4(0, 0, 0, 0);
         }
-        scale[q][0] = prmt(h, h, 0x1010);
-        scale[q][1] = prmt(h, h, 0x3232);
       }
-    }
+    };
+    // eight rows' scale words as the lane's two factors
+    const auto scales_of = [&](uint32_t word, bool in, float& f0, float& f1) {
+      if constexpr (FORMAT == kMxfp4) {
+        f0 = f1 = mx4_scale_value<kMxfp4>(word >> (8 * t) & 0xFF);
+      } else {
+        uint32_t f;
+        asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(f) : "r"(in ? word >> (16 * (t & 1)) : 0));
+        const float2 v = h2_to_f2(f);
+        f0 = v.x, f1 = v.y;
+      }
+    };
+    Ring<S::kSlots> r;
+    int parity = 0, turn = 0;
+    bool ok = true;
+    for (int u = first; u < p.units && ok; u += step, parity ^= 1) {
+      float acc[2][kN][4] = {};
+      for (int s = s0; s < s1; ++s, r.next(), turn ^= 1) {
+        if (turn != set) continue;
+        const bool any = s * kStage + kw * kStep < p.K;
+        if (any) load_x(s);
+        ok = wait(&full[r.slot], r.phase, kSitePipeFull);
+        if (!ok) break;
+        if (any) {
+          const uint32_t at = ring + r.slot * S::kSlot;
+          uint32_t w[4][4], sw[4];  // rows rr + 8 h
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+          for (int h = 0; h < 4; ++h) {
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[h][0]), "=r"(w[h][1]), "=r"(w[h][2]), "=r"(w[h][3]) : "r"(at + from + h * 1024));
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sw[h]) : "r"(at + from_s + (u & 3) * 4 + h * 128));
+          }
+          const bool in = s * (kStage / 32) + kw * 4 + t < chunks;  // there may be no scales there
+          float f[4][2];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        uint32_t up[4], down[4];
-        const auto word = [&](const uint4& r) { return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w; };
-        decode_pairs<TYPE>(word(v.w[2 * m]), scale[2 * m][i >> 1], up);
-        decode_pairs<TYPE>(word(v.w[2 * m + 1]), scale[2 * m + 1][i >> 1], down);
+          for (int h = 0; h < 4; ++h) scales_of(sw[h], in, f[h][0], f[h][1]);
+          if constexpr (kOne) {
+            float sum[2][2][4] = {};
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          mma16816<TYPE>(acc[m][n], up[0], down[0], up[1], down[1], b[n][4 * i], b[n][4 * i + 1]);
-          mma16816<TYPE>(acc[m][n], up[2], down[2], up[3], down[3], b[n][4 * i + 2], b[n][4 * i + 3]);
-          if constexpr (kSplit) {
-            mma16816<TYPE>(acc[m][n], up[0], down[0], up[1], down[1], lo[n][4 * i], lo[n][4 * i + 1]);
-            mma16816<TYPE>(acc[m][n], up[2], down[2], up[3], down[3], lo[n][4 * i + 2], lo[n][4 * i + 3]);
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                uint32_t up[4], down[4];
+                decode_pairs<TYPE, false>(table, lane4, w[2 * m][i], 0, up);
+                decode_pairs<TYPE, false>(table, lane4, w[2 * m + 1][i], 0, down);
+                mma16816<TYPE>(sum[m][0], up[0], down[0], up[1], down[1], x[0][i].x, x[0][i].y);
+                mma16816<TYPE>(sum[m][1], up[2], down[2], up[3], down[3], x[0][i].z, x[0][i].w);
+              }
+            // columns 2 t, 2 t + 1: the lane's own blocks
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int m = h >> 1, c = 2 * (h & 1) + e;
+                acc[m][0][c] = fmaf(sum[m][0][c] + sum[m][1][c], f[h][e], acc[m][0][c]);
+              }
+          } else {
+            uint32_t scale[4][2];  // of the row's two 16-value halves, as pairs
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) scale[h][e] = f2_to_pair<TYPE>(f[h][e], f[h][e]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t b[kN][4], lo[kSplit ? kN : 1][4];
+#pragma unroll
+              for (int n = 0; n < kN; ++n) {
+                const uint32_t v[4] = {x[n][i].x, x[n][i].y, x[n][i].z, x[n][i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if constexpr (kSplit) split_pair(v[k], b[n][k], lo[n][k]);
+                  else b[n][k] = v[k];
+                }
+              }
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                uint32_t up[4], down[4];
+                decode_pairs<TYPE, true>(table, lane4, w[2 * m][i], scale[2 * m][i >> 1], up);
+                decode_pairs<TYPE, true>(table, lane4, w[2 * m + 1][i], scale[2 * m + 1][i >> 1], down);
+#pragma unroll
+                for (int n = 0; n < kN; ++n) {
+                  mma16816<TYPE>(acc[m][n], up[0], down[0], up[1], down[1], b[n][0], b[n][1]);
+                  mma16816<TYPE>(acc[m][n], up[2], down[2], up[3], down[3], b[n][2], b[n][3]);
+                  if constexpr (kSplit) {
+                    mma16816<TYPE>(acc[m][n], up[0], down[0], up[1], down[1], lo[n][0], lo[n][1]);
+                    mma16816<TYPE>(acc[m][n], up[2], down[2], up[3], down[3], lo[n][2], lo[n][3]);
+                  }
+                }
+              }
+            }
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[r.slot]);
       }
-  };
-
-  // two steps of weights in flight
-  Weights v0, v1;
-  load(v0, first);
-  load(v1, first + stride);
-  for (int s = first; s < steps; s += 2 * stride) {
-    multiply(v0, s);
-    load(v0, s + 2 * stride);
-    if (s + stride < steps) {
-      multiply(v1, s + stride);
-      load(v1, s + 3 * stride);
+      // ---- the unit's sums; the other half of `part` is still being read by slower warps
+      if constexpr (kOne) {  // the columns of a row are in its four lanes: all into column 0
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          float v = acc[h >> 1][0][2 * (h & 1)] + acc[h >> 1][0][2 * (h & 1) + 1];
+          v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+          v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+          if (t == 0) part[((parity * kWarps + warp) * kRows + h * 8 + rr) * kX] = v;
+        }
+      } else {
+        float* mine = part + (parity * kWarps + warp) * kRows * kX;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)  // row 16 m + 8 (e / 2) + rr, token 8 n + 2 t + e % 2
+              mine[(m * 16 + (e >> 1) * 8 + rr) * kX + n * 8 + 2 * t + (e & 1)] = acc[m][n][e];
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+      float* sums = part + parity * kWarps * kRows * kX;
+      for (int e = threadIdx.x; e < kRows * p.batch; e += kConsumers) {
+        const int row = e % kRows, token = e / kRows;
+        float* at = sums + row * kX + token;
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) sum += at[k * kRows * kX];
+        if (p.splits > 1) {
+          at[0] = sum;
+        } else if (u * kRows + row < p.N) {
+          const float bias = p.bias ? load_value<XT>(p.bias, u * kRows + row) : 0.0f;
+          store_value<XT>(p.y, static_cast<size_t>(token) * p.N + u * kRows + row, fmaf(sum, gamma, bias));
+        }
+      }
     }
   }
-
-  // ---- partial sums of the warps, then of the CTAs
-  float* mine = part + warp * 32 * kX;
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)  // row part 2 m + e / 2, row g, token 8 n + 2 t + e % 2
-        mine[((2 * m + (e >> 1)) * 8 + g) * kX + n * 8 + 2 * t + (e & 1)] = acc[m][n][e];
-  __syncthreads();
-  if (p.split_ctas > 1) {
-    if (p.split_warps > 1) {
-      // into the first warp's place; each element is read and written by one thread
-      for (int e = threadIdx.x; e < groups * 32 * kX; e += kThreads) {
-        float* at = part + e / (32 * kX) * p.split_warps * 32 * kX + e % (32 * kX);
-        float sum = at[0];
-        for (int w = 1; w < p.split_warps; ++w) sum += at[w * 32 * kX];
-        at[0] = sum;
-      }
-    }
+  if (p.splits > 1) {  // of the one unit
+    __syncwarp();
     cluster_sync();
-  }
-  const float factor = (FORMAT == kNvfp4 && TYPE == kF16 ? 16384.0f : 1.0f) * (p.gamma ? *p.gamma : 1.0f);
-  const uint32_t base = smem_addr(part);
-  for (int e = rank * kThreads + threadIdx.x; e < groups * 32 * p.batch; e += kThreads * p.split_ctas) {
-    const int r = e % 32, token = e / 32 % p.batch, gr = e / 32 / p.batch;
-    const int id = (blockIdx.x / p.split_ctas) * groups + gr;
-    const int row = (id >> 2) * 128 + (id & 3) * 8 + (r & 7) + (r >> 3) * 32;
-    if (row >= p.N) continue;
-    const int at = gr * p.split_warps * 32 * kX + r * kX + token;
-    float sum = 0.0f;
-    if (p.split_ctas > 1) {
-      for (int c = 0; c < p.split_ctas; ++c) {
+    const float gamma = p.gamma ? *p.gamma : 1.0f;
+    for (int e = rank * kThreads + threadIdx.x; e < kRows * p.batch; e += kThreads * p.splits) {
+      const int row = e % kRows, token = e / kRows;
+      if (first * kRows + row >= p.N) continue;
+      const uint32_t at = smem_addr(part + row * kX + token);
+      float sum = 0.0f;
+      for (int c = 0; c < p.splits; ++c) {
         float v;
         asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-                     : "=f"(v) : "r"(base + at * 4), "r"(c) : "memory");
+                     : "=f"(v) : "r"(at), "r"(c) : "memory");
         sum += v;
       }
-    } else {
-      for (int w = 0; w < p.split_warps; ++w) sum += part[at + w * 32 * kX];
+      const float bias = p.bias ? load_value<XT>(p.bias, first * kRows + row) : 0.0f;
+      store_value<XT>(p.y, static_cast<size_t>(token) * p.N + first * kRows + row, fmaf(sum, gamma, bias));
     }
-    const float bias = p.bias ? load_value<XT>(p.bias, row) : 0.0f;
-    store_value<XT>(p.y, static_cast<size_t>(token) * p.N + row, fmaf(sum, factor, bias));
+    cluster_sync();  // no CTA leaves while another reads its sums
   }
-  if (p.split_ctas > 1) cluster_sync();  // no CTA leaves while another reads its sums
 }
 
 template <int FORMAT, int XT, int NB>
-cudaError_t gemv_as(const Mx4Linear& c, cudaStream_t stream) {
+cudaError_t gemv_as(const Mx4Linear& c, uint32_t* status, cudaStream_t stream) {
+  using S = Shape<FORMAT, NB>;
+  EncodeTiledFn encode = encode_tiled();
+  if (!encode) return cudaErrorNotSupported;
+  CUtensorMap map;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.K / 2), static_cast<cuuint64_t>(c.w.rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.K / 2)};
+  const cuuint32_t box[2] = {kBox / 2, kRows}, ones[2] = {1, 1};
+  if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(c.w.packed), dims, strides, box, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   GemvParams p{};
-  p.packed = c.w.packed;
   p.scales = c.w.scales;
   p.gamma = c.w.tensor_scale;
   p.x = c.x;
   p.bias = c.bias;
   p.y = c.y;
+  p.status = status;
   p.N = c.w.rows;
   p.K = c.K;
   p.batch = c.batch;
   p.tiles = mx4_scale_tiles(c.K, FORMAT);
-  // all warps of a CTA on one row group, then clusters, until there are CTAs for the SMs
-  const int steps = (c.K + kStep - 1) / kStep;
-  const long long row_groups = (static_cast<long long>(c.w.rows) + 127) / 128 * 4;
-  p.split_warps = kWarps;
-  while (p.split_warps > 1 && (steps < 2 * p.split_warps || row_groups / (kWarps / p.split_warps) >= 16 * kSms)) p.split_warps /= 2;
-  p.split_ctas = 1;
-  const int groups = kWarps / p.split_warps;
-  const long long ctas = (row_groups + groups - 1) / groups;
-  while (p.split_ctas < 8 && ctas * p.split_ctas < kSms && steps >= 4 * p.split_warps * p.split_ctas) p.split_ctas *= 2;
-  return launch_overlapped(gemv_kernel<FORMAT, XT, NB>, static_cast<unsigned>(ctas * p.split_ctas), kThreads, 0, stream,
-                           p.split_ctas, p);
+  p.units = (c.w.rows + kRows - 1) / kRows;
+  p.splits = 1;
+  while (p.splits < 8 && p.units * p.splits * 2 <= kSms && (c.K + kStage - 1) / kStage >= p.splits * 2) p.splits *= 2;
+  auto* kernel = gemv_kernel<FORMAT, XT, NB>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
+  if (e != cudaSuccess) return e;
+  const int ctas = p.units * p.splits;
+  return launch_overlapped(kernel, p.splits > 1 || ctas < kSms ? ctas : kSms, kThreads, S::kSmem, stream, p.splits, map, p);
 }
 
 template <int FORMAT, int XT>
-cudaError_t gemv_tokens(const Mx4Linear& c, cudaStream_t stream) {
-  if (c.batch <= 8) return gemv_as<FORMAT, XT, 1>(c, stream);
-  if (c.batch <= 16) return gemv_as<FORMAT, XT, 2>(c, stream);
-  return gemv_as<FORMAT, XT, 4>(c, stream);
+cudaError_t gemv_tokens(const Mx4Linear& c, uint32_t* status, cudaStream_t stream) {
+  if (c.batch == 1) return gemv_as<FORMAT, XT, 0>(c, status, stream);
+  if (c.batch <= 8) return gemv_as<FORMAT, XT, 1>(c, status, stream);
+  return gemv_as<FORMAT, XT, 2>(c, status, stream);
 }
 
 }  // namespace
 
-bool mx4_gemv_takes(int batch) { return batch <= 32; }
+bool mx4_gemv_takes(int batch) { return batch <= 16; }
 
-cudaError_t launch_mx4_gemv(const Mx4Linear& c, cudaStream_t stream) {
-  if (c.format == kMxfp4) return c.type == kF16 ? gemv_tokens<kMxfp4, kF16>(c, stream) : gemv_tokens<kMxfp4, kBf16>(c, stream);
-  return c.type == kF16 ? gemv_tokens<kNvfp4, kF16>(c, stream) : gemv_tokens<kNvfp4, kBf16>(c, stream);
+cudaError_t launch_mx4_gemv(const Mx4Linear& c, uint32_t* status, cudaStream_t stream) {
+  if (c.format == kMxfp4) return c.type == kF16 ? gemv_tokens<kMxfp4, kF16>(c, status, stream) : gemv_tokens<kMxfp4, kBf16>(c, status, stream);
+  return c.type == kF16 ? gemv_tokens<kNvfp4, kF16>(c, status, stream) : gemv_tokens<kNvfp4, kBf16>(c, status, stream);
 }
 
 }  // namespace aqlm

@@ -43,7 +43,7 @@ struct Mx4Linear {
 cudaError_t launch_mx4_linear(const Mx4Linear& p, uint32_t* status, cudaStream_t stream);
 // The kernel for a few tokens, and whether a batch is one for it.
 bool mx4_gemv_takes(int batch);
-cudaError_t launch_mx4_gemv(const Mx4Linear& p, cudaStream_t stream);
+cudaError_t launch_mx4_gemv(const Mx4Linear& p, uint32_t* status, cudaStream_t stream);
 size_t mx4_linear_workspace(int type, int format, long long K, long long batch);
 
 // y = x . W^T with both operands in 4 bits.

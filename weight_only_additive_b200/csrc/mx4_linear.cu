@@ -628,7 +628,7 @@ size_t mx4_grad_workspace(int type, int format, long long N, long long batch) {
 }
 
 cudaError_t launch_mx4_linear(const Mx4Linear& p, uint32_t* status, cudaStream_t stream) {
-  if (mx4_gemv_takes(p.batch)) return launch_mx4_gemv(p, stream);
+  if (mx4_gemv_takes(p.batch)) return launch_mx4_gemv(p, status, stream);
   return run<false>(Call{p.x, p.w, p.bias, p.y, p.type, p.w.rows, p.K, p.K, p.batch, p.format, p.workspace}, status, stream);
 }
 
