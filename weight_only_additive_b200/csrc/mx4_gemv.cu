@@ -98,10 +98,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
   constexpr bool kSplit = !kOne && FORMAT == kMxfp4 && XT == kF16;
   constexpr int TYPE = kSplit ? kBf16 : XT;
   constexpr int kX = kN * 8;  // columns
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* table = smem_raw + (1024 - (smem_addr(smem_raw) & 1023));
+  extern __shared__ __align__(16) uint8_t table[];  // first, so that its address is a constant of the lookups
   float* part = reinterpret_cast<float*>(table + kTableBytes);  // [2][warps][32 rows][columns]
-  const uint32_t ring = smem_addr(table) + kTableBytes + S::kPart;
+  const uint32_t ring = (smem_addr(table) + kTableBytes + S::kPart + 1023) & ~1023u;
   __shared__ uint64_t full[S::kSlots], empty[S::kSlots];
   __shared__ volatile uint32_t failed;
 
