@@ -23,7 +23,7 @@ class Format(enum.IntEnum):
 
     @property
     def block(self) -> int:
-        return 32 if self == Format.MXFP4 else 16
+        return 16 if self else 32
 
 
 _TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
@@ -38,7 +38,7 @@ def _type(dtype, name: str, wide: bool = False) -> int:
 
 def scale_tiles(rows: int, K: int, format: Format):
     """Shape of the tiled scales of a rows x K tensor: [row tiles, tiles along K, 512]."""
-    return -(-rows // 128), -(-K // (4 * Format(format).block)), 512
+    return (rows + 127) // 128, -(-K // (4 * Format(format).block)), 512
 
 
 @dataclass
@@ -52,7 +52,8 @@ class Mx4Tensor:
     def __post_init__(self):
         # the kernels read exactly the sizes that rows, K and the format imply
         p, s, g = self.packed, self.scales, self.tensor_scale
-        self.format = Format(self.format)
+        if type(self.format) is not Format:
+            self.format = Format(self.format)
         if p.dim() != 2 or p.shape[1] == 0 or p.shape[1] % 16 or p.shape[0] == 0:
             raise ValueError(f"packed must be [rows, K/2] with K a multiple of 32, got shape {tuple(p.shape)}")
         dev = p.device
@@ -62,6 +63,13 @@ class Mx4Tensor:
             _check_tensor(g, "tensor_scale", torch.float32, dev)
             if g.numel() != 1:
                 raise ValueError(f"tensor_scale must hold one value, got shape {tuple(g.shape)}")
+
+    @classmethod
+    def _of(cls, packed, scales, format, tensor_scale) -> "Mx4Tensor":
+        """Of tensors made here, which need no checks."""
+        t = object.__new__(cls)
+        t.packed, t.scales, t.format, t.tensor_scale = packed, scales, format, tensor_scale
+        return t
 
     @property
     def rows(self) -> int:
@@ -101,33 +109,39 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-class _On:
-    """The device and stream of one call: the library launches on the current device, and
-    what the call allocates belongs to the stream that it runs on."""
+def _check(status: int, what: str):
+    if status:
+        raise native.AqlmError(status, what)
 
-    def __init__(self, t: torch.Tensor, stream: Optional[torch.cuda.Stream]):
-        dev = t.device
-        if dev.type != "cuda":
-            raise ValueError(f"mx4 tensors must live on a CUDA device, got {dev}")
-        self.guard = None
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-            self.guard = torch.cuda.stream(stream)  # sets the device too
-        elif dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(dev)
-        self.stream = stream
-        self.device = dev
 
-    def __enter__(self) -> int:
-        if self.guard is not None:
-            self.guard.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        return s.cuda_stream
+class _Here:
+    """No change of device or stream."""
+
+    def __enter__(self):
+        pass
 
     def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        pass
+
+
+_HERE = _Here()
+
+
+def _on(dev: torch.device, stream: Optional[torch.cuda.Stream]):
+    """The context that a call runs in: the library launches on the current device, and what
+    a call allocates belongs to the stream that it runs on."""
+    if dev.type != "cuda":
+        raise ValueError(f"mx4 tensors must live on a CUDA device, got {dev}")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)  # sets the device too
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+# The handle of a device's current stream (torch.cuda.current_stream builds an object, which
+# takes as long as a small kernel).
+_current = torch._C._cuda_getCurrentRawStream
 
 
 def _matrix(t: torch.Tensor, name: str, cols: Optional[int], what: str, dev):
@@ -146,24 +160,28 @@ def quantize(x: torch.Tensor, format: Format, tensor_scale: Optional[torch.Tenso
     max|x| / 2688, which puts the largest value at the top of the format.
     out: an Mx4Tensor of the same rows, K and format to write into (its own
     tensor_scale must be the call's).  Rounding and NaN: include/mx4.h."""
-    fmt = Format(format)
-    _matrix(x, "x", None, "K", x.device)
+    fmt = format if type(format) is Format else Format(format)
+    dev = x.device
+    _matrix(x, "x", None, "K", dev)
     xt = _type(x.dtype, "x", wide=True)
     rows, K = x.shape
     if rows == 0 or K == 0 or K % 32:
         raise ValueError(f"x must have at least one row and K a multiple of 32, got shape {tuple(x.shape)}")
-    if fmt == Format.MXFP4 and tensor_scale is not None:
-        raise ValueError("MXFP4 is quantised without a tensor scale")
-    with _On(x, stream) as s:
+    if tensor_scale is not None:
+        if fmt == Format.MXFP4:
+            raise ValueError("MXFP4 is quantised without a tensor scale")
+        _check_tensor(tensor_scale, "tensor_scale", torch.float32, dev)
+        if tensor_scale.numel() != 1:
+            raise ValueError(f"tensor_scale must hold one value, got shape {tuple(tensor_scale.shape)}")
+    with _on(dev, stream):
         if out is None:
-            packed = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
-            scales = torch.empty(scale_tiles(rows, K, fmt), dtype=torch.uint8, device=x.device)
-            out = Mx4Tensor(packed, scales, fmt, tensor_scale)
-        elif (out.rows, out.K, out.format, out.device) != (rows, K, fmt, x.device) or \
+            out = Mx4Tensor._of(torch.empty((rows, K // 2), dtype=torch.uint8, device=dev),
+                                torch.empty(scale_tiles(rows, K, fmt), dtype=torch.uint8, device=dev), fmt, tensor_scale)
+        elif (out.rows, out.K, out.format, out.device) != (rows, K, fmt, dev) or \
                 _ptr(out.tensor_scale) != _ptr(tensor_scale):
             raise ValueError("out must have x's rows and K, its device, the format and the tensor scale of the call")
-        native.mx4_quantize(x.data_ptr(), xt, out.packed.data_ptr(), out.scales.data_ptr(), _ptr(tensor_scale), rows, K,
-                            fmt, s)
+        _check(native.lib().mx4_quantize(x.data_ptr(), xt, out.packed.data_ptr(), out.scales.data_ptr(),
+                                         _ptr(tensor_scale), rows, K, fmt, _current(dev.index)), "mx4_quantize")
     return out
 
 
@@ -171,13 +189,17 @@ def dequantize(t: Mx4Tensor, dtype: torch.dtype = torch.float16, out: Optional[t
                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The tensor's values [rows, K] in fp16, bf16 or fp32: computed in fp32, rounded once."""
     code = _type(dtype, "dtype", wide=True)
-    with _On(t.packed, stream) as s:
+    packed = t.packed
+    dev = packed.device
+    rows, half = packed.shape
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty((t.rows, t.K), dtype=dtype, device=t.device)
+            out = torch.empty((rows, 2 * half), dtype=dtype, device=dev)
         else:
-            _check_tensor(out, "out", dtype, t.device, (t.rows, t.K))
-        native.mx4_dequantize(t.packed.data_ptr(), t.scales.data_ptr(), _ptr(t.tensor_scale), out.data_ptr(), code,
-                              t.rows, t.K, t.format, s)
+            _check_tensor(out, "out", dtype, dev, (rows, 2 * half))
+        _check(native.lib().mx4_dequantize(packed.data_ptr(), t.scales.data_ptr(), _ptr(t.tensor_scale),
+                                           out.data_ptr(), code, rows, 2 * half, t.format, _current(dev.index)),
+               "mx4_dequantize")
     return out
 
 
@@ -188,11 +210,13 @@ def matmul(x: Union[torch.Tensor, Mx4Tensor], w: Mx4Tensor, bias: Optional[torch
 
     x: a [batch, K] fp16 or bf16 tensor (weights taken exactly; y in x's type), or an
     Mx4Tensor of w's format, whose product runs on the block-scaled tensor-core path (y
-    in out_dtype: fp16, bf16 or fp32; bias's type if None, else fp16).
+    in out_dtype: fp16, bf16 or fp32; out's or bias's type if None, else fp16).
     bias: [N] in y's type."""
     four = isinstance(x, Mx4Tensor)
-    dev = w.device
-    N, K = w.rows, w.K
+    packed = w.packed
+    dev = packed.device
+    N, half = packed.shape
+    K = 2 * half
     if four:
         if x.device != dev:
             raise ValueError(f"x must be on {dev}, got {x.device}")
@@ -215,20 +239,24 @@ def matmul(x: Union[torch.Tensor, Mx4Tensor], w: Mx4Tensor, bias: Optional[torch
         out_dtype = x.dtype
     if bias is not None:
         _check_tensor(bias, "bias", out_dtype, dev, (N,))
-    with _On(w.packed, stream) as s:
+    with _on(dev, stream):
         if out is None:
             out = torch.empty((batch, N), dtype=out_dtype, device=dev)
         else:
             _check_tensor(out, "out", out_dtype, dev, (batch, N))
         if four:
-            native.mx4_matmul_mx4(x.packed.data_ptr(), x.scales.data_ptr(), _ptr(x.tensor_scale), w.packed.data_ptr(),
-                                  w.scales.data_ptr(), _ptr(w.tensor_scale), _ptr(bias), out.data_ptr(), code, N, K,
-                                  batch, w.format, s)
+            _check(native.lib().mx4_matmul_mx4(x.packed.data_ptr(), x.scales.data_ptr(), _ptr(x.tensor_scale),
+                                               packed.data_ptr(), w.scales.data_ptr(), _ptr(w.tensor_scale),
+                                               _ptr(bias), out.data_ptr(), code, N, K, batch, w.format,
+                                               _current(dev.index)), "mx4_matmul_mx4")
         else:
-            need = native.mx4_matmul_workspace_size(code, N, K, batch, w.format)
-            ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-            native.mx4_matmul(x.data_ptr(), code, w.packed.data_ptr(), w.scales.data_ptr(), _ptr(w.tensor_scale),
-                              _ptr(bias), out.data_ptr(), N, K, batch, w.format, _ptr(ws), need, s)
+            ws, need = None, 0
+            if code == 0 and not w.format:  # fp16 x with MXFP4 weights alone can need one
+                need = native.mx4_matmul_workspace_size(code, N, K, batch, w.format)
+                ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+            _check(native.lib().mx4_matmul(x.data_ptr(), code, packed.data_ptr(), w.scales.data_ptr(),
+                                           _ptr(w.tensor_scale), _ptr(bias), out.data_ptr(), N, K, batch, w.format,
+                                           _ptr(ws), need, _current(dev.index)), "mx4_matmul")
     return out
 
 
@@ -236,20 +264,22 @@ def input_grad(dy: torch.Tensor, w: Mx4Tensor, out: Optional[torch.Tensor] = Non
                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """dx = dy . W [batch, K] for dy [batch, N] fp16 or bf16: the gradient of matmul() with
     respect to 16-bit x (the weights are fixed, and taken exactly)."""
-    dev = w.device
-    N, K = w.rows, w.K
+    packed = w.packed
+    dev = packed.device
+    N, half = packed.shape
     _matrix(dy, "dy", N, "N", dev)
     code = _type(dy.dtype, "dy")
     batch = dy.shape[0]
     if batch == 0:
         raise ValueError("dy must have at least one row")
-    with _On(w.packed, stream) as s:
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty((batch, K), dtype=dy.dtype, device=dev)
+            out = torch.empty((batch, 2 * half), dtype=dy.dtype, device=dev)
         else:
-            _check_tensor(out, "out", dy.dtype, dev, (batch, K))
-        need = native.mx4_input_grad_workspace_size(code, N, K, batch, w.format)
+            _check_tensor(out, "out", dy.dtype, dev, (batch, 2 * half))
+        need = native.mx4_input_grad_workspace_size(code, N, 2 * half, batch, w.format)
         ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-        native.mx4_input_grad(dy.data_ptr(), code, w.packed.data_ptr(), w.scales.data_ptr(), _ptr(w.tensor_scale),
-                              out.data_ptr(), N, K, batch, w.format, _ptr(ws), need, s)
+        _check(native.lib().mx4_input_grad(dy.data_ptr(), code, packed.data_ptr(), w.scales.data_ptr(),
+                                           _ptr(w.tensor_scale), out.data_ptr(), N, 2 * half, batch, w.format,
+                                           _ptr(ws), need, _current(dev.index)), "mx4_input_grad")
     return out
