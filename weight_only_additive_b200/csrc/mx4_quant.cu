@@ -8,13 +8,25 @@ namespace aqlm {
 namespace {
 
 constexpr int kThreads = 256;
-// Grid-stride beyond this many CTAs.
-constexpr long long kMaxBlocks = 148LL * 64;
+constexpr int kSms = 148;
 
-// idx / units, in 32 bits where the total allows it.
-__device__ __forceinline__ long long row_of(long long idx, int units, bool small) {
-  return small ? static_cast<long long>(static_cast<uint32_t>(idx) / static_cast<uint32_t>(units)) : idx / units;
-}
+// A thread's way through rows of `units` pieces, `stride` pieces at a time: one division at
+// the start, then additions.
+struct Walk {
+  int row, u;  // piece u of a row
+  int rows_on, units_on, units;
+  __device__ __forceinline__ Walk(long long first, long long stride, int units_) : units(units_) {
+    row = static_cast<int>(first / units);
+    u = static_cast<int>(first - static_cast<long long>(row) * units);
+    rows_on = static_cast<int>(stride / units);
+    units_on = static_cast<int>(stride - static_cast<long long>(rows_on) * units);
+  }
+  __device__ __forceinline__ void next() {
+    row += rows_on;
+    u += units_on;
+    if (u >= units) u -= units, ++row;
+  }
+};
 
 // 32 bytes at p (16-byte aligned; `wide`: 32-byte aligned).
 __device__ __forceinline__ void load32(const void* p, bool wide, uint32_t (&v)[8]) {
@@ -61,7 +73,7 @@ __device__ __forceinline__ uint32_t to_e4m3(float v) {
 
 // The e2m1 code of x / unit from exact products in 64 bits (a midpoint has 3 bits, the
 // unit at most 28): one more for every midpoint below |x|, ties to the even code.
-__device__ __noinline__ uint32_t exact_e2m1(float x, double unit) {
+__device__ __forceinline__ uint32_t exact_e2m1(float x, double unit) {
   const double a = fabs(static_cast<double>(x));
   uint32_t code = 0;
 #pragma unroll
@@ -73,13 +85,26 @@ __device__ __noinline__ uint32_t exact_e2m1(float x, double unit) {
   return code | (__float_as_uint(x) >> 31 << 3);
 }
 
-// e4m3 of the exact quotient amax / (6 gamma), inv = 1 / (6 gamma) to 64 bits.  The
-// 64-bit product is within 2^-51 of the quotient; a quotient that is not a tie stays
-// 2^-33 away from every tie (its terms have 24 and 27 bits), so what lies within 2^-40
-// of an fp32 value is that value, and anything else goes to the odd fp32 neighbour: the
-// conversion then rounds it as it would the quotient.
-__device__ __forceinline__ uint32_t scale_e4m3(float amax, double inv) {
-  const double v = fmin(static_cast<double>(amax) * inv, 1024.0);
+// `codes` of the eight values at x, those whose nibble is set in `doubt` decided exactly.
+// Rare, so out of the way of the registers and instructions of the common path.
+template <int TYPE>
+__device__ __noinline__ uint32_t settle(const void* x, uint32_t codes, uint32_t doubt, float s, float gamma) {
+  const double unit = static_cast<double>(s) * static_cast<double>(gamma);
+  while (doubt) {
+    const int i = (__ffs(doubt) - 1) >> 2;
+    const uint32_t at = 0xFu << (4 * i);
+    codes = (codes & ~at) | exact_e2m1(load_value<TYPE>(x, i), unit) << (4 * i);
+    doubt &= ~at;
+  }
+  return codes;
+}
+
+// e4m3 of the exact quotient amax / (6 gamma) where fp32 leaves it open.  The 64-bit quotient
+// is within 2^-52 of it; one that is not a tie stays 2^-33 away from every tie (its terms have
+// 24 and 27 bits), so what lies within 2^-40 of an fp32 value is that value, and anything else
+// goes to the odd fp32 neighbour: the conversion then rounds it as it would the quotient.
+__device__ __noinline__ uint32_t settle_scale(float amax, float gamma) {
+  const double v = fmin(static_cast<double>(amax) / (6.0 * static_cast<double>(gamma)), 1024.0);
   const float f = __double2float_rn(v);
   const double r = v - static_cast<double>(f);
   uint32_t bits = __float_as_uint(f);
@@ -138,26 +163,33 @@ struct Values {
 
 // Rows of `units` 16-value pieces, the last ones past K filling the row's last scale tile.
 template <int FORMAT, int TYPE>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const void* __restrict__ x, uint8_t* __restrict__ packed,
+__global__ void __launch_bounds__(kThreads, TYPE == kF32 ? 4 : 5) quantize_kernel(const void* __restrict__ x, uint8_t* __restrict__ packed,
                                                             uint8_t* __restrict__ scales,
-                                                            const float* __restrict__ tensor_scale, long long total,
-                                                            int units, int K, int tiles, bool small, bool wide) {
+                                                            const float* __restrict__ tensor_scale, int rows,
+                                                            int units, int K, int tiles, bool wide) {
   grid_dependency_wait();
   grid_dependents_launch();
   const float gamma = FORMAT == kNvfp4 && tensor_scale ? *tensor_scale : 1.0f;
   const bool gamma_bad = !(gamma >= 0.0f && gamma <= 3.402823466e38f);
-  const double inv6 = gamma > 0.0f ? 1.0 / (6.0 * static_cast<double>(gamma)) : 0.0;
+  // 1 / (6 gamma), or 0 where fp32 cannot hold it well
+  const float inv6 = gamma > 0x1p-120f && gamma < 0x1p100f ? 1.0f / (6.0f * gamma) : 0.0f;
   const int lane = threadIdx.x & 31;
-  const long long stride = static_cast<long long>(gridDim.x) * kThreads;
-  for (long long base = static_cast<long long>(blockIdx.x) * kThreads + (threadIdx.x & ~31); base < total;
-       base += stride) {
-    const long long idx = base + lane;
-    const long long row = row_of(idx < total ? idx : 0, units, small);
-    const int u = static_cast<int>(idx - row * units);
-    const bool inside = idx < total && u * 16 < K;
-    Values<TYPE> v;
-    if (inside) v.load(x, static_cast<size_t>(row) * K + static_cast<size_t>(u) * 16, wide);
+  // the next piece is loaded before this one is converted; the lanes of a warp, whose pieces
+  // are neighbours, go on together while any has one
+  Walk way(static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x, static_cast<long long>(gridDim.x) * kThreads, units);
+  const auto fetch = [&](Values<TYPE>& v) {
+    if (way.row < rows && way.u * 16 < K) v.load(x, static_cast<size_t>(way.row) * K + static_cast<size_t>(way.u) * 16, wide);
     else v.zero();
+  };
+  Values<TYPE> ahead;
+  fetch(ahead);
+  while (__any_sync(0xFFFFFFFFu, way.row < rows)) {
+    const Values<TYPE> v = ahead;
+    const int row = way.row, u = way.u;
+    const bool inside = row < rows && u * 16 < K;
+    const size_t at = static_cast<size_t>(row) * K + static_cast<size_t>(u) * 16;
+    way.next();
+    fetch(ahead);
     uint32_t top = v.amax_bits();
     if (FORMAT == kMxfp4) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     const bool bad = top >= (TYPE == kF32 ? 0x7F800000u : TYPE == kBf16 ? 0x7F80u : 0x7C00u);
@@ -182,16 +214,21 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const void* __restri
         code = 0xFF;
       }
     } else {
-      code = scale_e4m3(amax, inv6);
+      // fp32 quotients are within 2^-21; where that much to either side gives two codes, or
+      // fp32 cannot hold them, the exact comparison decides
+      const float v6 = amax * inv6;
+      uint32_t both;
+      asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}"
+          : "=r"(both) : "f"(v6 * (1.0f + 0x1p-20f)), "f"(v6 * (1.0f - 0x1p-20f)));
+      code = both & 0xFF;
+      if ((both >> 8 != code || inv6 == 0.0f) && gamma > 0.0f) code = settle_scale(amax, gamma);
       if (bad || gamma_bad) {
         code = 0x7F;
       } else if (code != 0) {
-        // fp32 quotients are within 2^-21; where that much to either side gives two
-        // codes, the exact comparison decides
         const float s = mx4_scale_value<kNvfp4>(code);
         const float unit = s * gamma;
         const bool plain = unit > 0x1p-100f && unit < 0x1p100f;
-        const float inv = plain ? __fdividef(1.0f, unit) : 0.0f;
+        const float inv = __fdividef(1.0f, unit);
         const float below = inv * (1.0f - 0x1p-20f), above = inv * (1.0f + 0x1p-20f);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -203,19 +240,14 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const void* __restri
 #pragma unroll
           for (int i = 0; i < 8; ++i) g[i] = f[i] * below;
           uint32_t lo = to_e2m1x8(g);
-          const uint32_t differ = plain ? hi ^ lo : 0xFFFFFFFFu;
-          if (differ) {
-            const double exact_unit = static_cast<double>(s) * static_cast<double>(gamma);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (differ >> (4 * i) & 0xF)
-                lo = (lo & ~(0xFu << (4 * i))) | exact_e2m1(f[i], exact_unit) << (4 * i);
-          }
+          const uint32_t doubt = plain ? hi ^ lo : 0xFFFFFFFFu;
+          if (doubt && inside)
+            lo = settle<TYPE>(static_cast<const uint8_t*>(x) + (at + 8 * h) * (TYPE == kF32 ? 4 : 2), lo, doubt, s, gamma);
           (h ? q.y : q.x) = lo;
         }
       }
     }
-    if (inside) *reinterpret_cast<uint2*>(packed + (static_cast<size_t>(row) * K + static_cast<size_t>(u) * 16) / 2) = q;
+    if (inside) *reinterpret_cast<uint2*>(packed + at / 2) = q;
 
     // the four scales of a tile's row together
     if (!inside) code = 0;
@@ -223,8 +255,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const void* __restri
     uint32_t four = code << (8 * ((lane / kPer) & 3));
     four |= __shfl_xor_sync(0xFFFFFFFFu, four, kPer);
     four |= __shfl_xor_sync(0xFFFFFFFFu, four, 2 * kPer);
-    if (idx < total && (lane & (4 * kPer - 1)) == 0)
-      *reinterpret_cast<uint32_t*>(scales + mx4_scale_at(static_cast<int>(row), u / kPer, tiles)) = four;
+    if (row < rows && (lane & (4 * kPer - 1)) == 0)
+      *reinterpret_cast<uint32_t*>(scales + mx4_scale_at(row, u / kPer, tiles)) = four;
   }
 }
 
@@ -233,26 +265,26 @@ template <int FORMAT, int TYPE>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* __restrict__ packed,
                                                               const uint8_t* __restrict__ scales,
                                                               const float* __restrict__ tensor_scale,
-                                                              void* __restrict__ out, long long total, int units,
-                                                              int tiles, bool small, bool wide) {
+                                                              void* __restrict__ out, int rows, int units, int tiles,
+                                                              bool wide) {
   grid_dependency_wait();
   grid_dependents_launch();
   const float gamma = tensor_scale ? *tensor_scale : 1.0f;
-  const long long stride = static_cast<long long>(gridDim.x) * kThreads;
-  for (long long idx = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; idx < total; idx += stride) {
-    const long long row = row_of(idx, units, small);
-    const int u = static_cast<int>(idx - row * units);
-    const uint4 w = ldg_nc_v4(packed + static_cast<size_t>(idx) * 16);
+  Walk way(static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x, static_cast<long long>(gridDim.x) * kThreads, units);
+  for (; way.row < rows; way.next()) {
+    const int row = way.row, u = way.u;
+    const size_t idx = static_cast<size_t>(row) * units + u;
+    const uint4 w = ldg_nc_v4(packed + idx * 16);
     float s[2];
     if constexpr (FORMAT == kMxfp4) {
-      s[0] = s[1] = mx4_scale_value<FORMAT>(scales[mx4_scale_at(static_cast<int>(row), u, tiles)]);
+      s[0] = s[1] = mx4_scale_value<FORMAT>(scales[mx4_scale_at(row, u, tiles)]);
     } else {
-      const uint32_t two = *reinterpret_cast<const uint16_t*>(scales + mx4_scale_at(static_cast<int>(row), 2 * u, tiles));
+      const uint32_t two = *reinterpret_cast<const uint16_t*>(scales + mx4_scale_at(row, 2 * u, tiles));
       s[0] = mx4_scale_value<FORMAT>(two & 0xFF);
       s[1] = mx4_scale_value<FORMAT>(two >> 8);
     }
     const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-    uint8_t* o = static_cast<uint8_t*>(out) + static_cast<size_t>(idx) * 32 * (TYPE == kF32 ? 4 : 2);
+    uint8_t* o = static_cast<uint8_t*>(out) + idx * 32 * (TYPE == kF32 ? 4 : 2);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t v[TYPE == kF32 ? 16 : 8];
@@ -283,9 +315,10 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* __r
   }
 }
 
-unsigned blocks_for(long long total) {
-  const long long b = (total + kThreads - 1) / kThreads;
-  return static_cast<unsigned>(b < kMaxBlocks ? b : kMaxBlocks);
+// CTAs for `total` pieces, at most `most` an SM.
+unsigned blocks_for(long long total, int most) {
+  const long long b = (total + kThreads - 1) / kThreads, cap = static_cast<long long>(kSms) * most;
+  return static_cast<unsigned>(b < cap ? b : cap);
 }
 
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
@@ -296,17 +329,16 @@ cudaError_t quantize_as(const void* x, uint8_t* packed, uint8_t* scales, const f
   const int tiles = mx4_scale_tiles(K, FORMAT);
   const int units = tiles * 4 * mx4_block(FORMAT) / 16;
   const long long total = static_cast<long long>(rows) * units;
-  return launch_overlapped(quantize_kernel<FORMAT, TYPE>, blocks_for(total), kThreads, 0, stream, 1, x, packed, scales,
-                           tensor_scale, total, units, K, tiles, total <= 0xFFFFFFFFll, aligned32(x));
+  return launch_overlapped(quantize_kernel<FORMAT, TYPE>, blocks_for(total, TYPE == kF32 ? 4 : 5), kThreads, 0, stream, 1,
+                           x, packed, scales, tensor_scale, rows, units, K, tiles, aligned32(x));
 }
 
 template <int FORMAT, int TYPE>
 cudaError_t dequantize_as(const Mx4& t, void* out, int K, cudaStream_t stream) {
   const int units = K / 32;
   const long long total = static_cast<long long>(t.rows) * units;
-  return launch_overlapped(dequantize_kernel<FORMAT, TYPE>, blocks_for(total), kThreads, 0, stream, 1, t.packed,
-                           t.scales, t.tensor_scale, out, total, units, mx4_scale_tiles(K, FORMAT),
-                           total <= 0xFFFFFFFFll, aligned32(out));
+  return launch_overlapped(dequantize_kernel<FORMAT, TYPE>, blocks_for(total, 64), kThreads, 0, stream, 1, t.packed,
+                           t.scales, t.tensor_scale, out, t.rows, units, mx4_scale_tiles(K, FORMAT), aligned32(out));
 }
 
 }  // namespace
