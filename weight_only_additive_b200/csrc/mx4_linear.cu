@@ -26,12 +26,17 @@ constexpr int kF = 128;          // features of a CTA
 constexpr int kSlotDepth = 256;  // reduction depth of a weight slot
 constexpr int kRing = 4;         // stages in flight
 constexpr int kSlotBytes = 16384, kSlotScales = 2048;
-constexpr int kWarpX = 0, kWarpMma = 1, kWarpDecode = 2, kWarpOut = 10, kWarpW = 14;
-constexpr int kThreads = 15 * 32;
+constexpr int kTableBytes = 65536;
 constexpr int kSms = 148;
 
-template <bool GRAD>
+// TABLE: decoding by lookup, for the tiles of few tokens, where decoding is what takes the
+// time (11008 x 4096 and 37 tokens: 24.6 us without, 18.9 with); their small stages leave room
+// for the table.
+template <bool GRAD, bool TABLE>
 struct Shape {
+  static constexpr int kGroups = TABLE ? 4 : 2;  // of four decoding warps, which take stages in turn
+  static constexpr int kWarpX = 0, kWarpMma = 1, kWarpDecode = 2, kWarpOut = 2 + 4 * kGroups, kWarpW = kWarpOut + 4;
+  static constexpr int kThreads = (kWarpW + 1) * 32;
   // Reduction depth of a stage.  Every stage costs the MMA thread a wait and a commit, so
   // deep ones; dx's decoded stages lie in shared memory, which has room for 64.
   static constexpr int kDepth = GRAD ? 64 : 128;
@@ -39,11 +44,12 @@ struct Shape {
   static constexpr int kABytes = GRAD ? kF * kDepth * 2 : 0;
   static constexpr uint32_t kACols = kDepth / 2;  // TMEM columns of a decoded stage (not GRAD)
   static constexpr int kWSlots = GRAD ? 3 : 4;
-  static constexpr int kXBytes = (GRAD ? 96 : 128) * 1024;
+  static constexpr int kXBytes = (TABLE ? GRAD ? 32 : 64 : GRAD ? 96 : 128) * 1024;
   static constexpr int kX = kRing * kABytes;
   static constexpr int kW = kX + kXBytes;
   static constexpr int kS = kW + kWSlots * kSlotBytes;
-  static constexpr size_t kSmem = kS + kWSlots * kSlotScales + 1024;
+  static constexpr size_t kSmem = (TABLE ? kTableBytes : 0) + kS + kWSlots * kSlotScales + 1024;
+  static_assert(kRing % kGroups == 0, "");
 };
 constexpr uint32_t kATmem = 256;  // first TMEM column of the decoded stages
 
@@ -124,10 +130,17 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t b) {
   }
 }
 
-// Eight codes times the scale as four pairs.
-template <int TYPE>
-__device__ __forceinline__ void decode_scaled(uint32_t codes, uint32_t scale, uint32_t (&h)[4]) {
-  e2m1x8_decode<TYPE>(codes, h);
+// Eight codes times the scale as four pairs.  TABLE: a byte of two codes is looked up in the
+// lane's copy of the table (256 bytes a row, a bank a lane; lane4 = 4 * lane).
+template <int TYPE, bool TABLE>
+__device__ __forceinline__ void decode_scaled(const uint8_t* table, uint32_t lane4, uint32_t codes, uint32_t scale,
+                                              uint32_t (&h)[4]) {
+  if constexpr (TABLE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const uint32_t*>(table + prmt(codes, lane4, 0x5504 | i << 4));
+  } else {
+    e2m1x8_decode<TYPE>(codes, h);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = TYPE == kF16 ? hmul2(h[i], scale) : bmul2(h[i], scale);
 }
@@ -156,14 +169,16 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return v;
 }
 
-template <int FORMAT, int TYPE, bool GRAD, int CG>
-__global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ CUtensorMap x_map,
+template <int FORMAT, int TYPE, bool GRAD, int CG, bool TABLE>
+__global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel(const __grid_constant__ CUtensorMap x_map,
                                                              const __grid_constant__ CUtensorMap w_map,
                                                              const LinearParams p) {
-  using S = Shape<GRAD>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t smem = (smem_addr(smem_raw) + 1023) & ~1023u;
-  uint8_t* smem_ptr = smem_raw + (smem - smem_addr(smem_raw));
+  using S = Shape<GRAD, TABLE>;
+  constexpr int kWarpX = S::kWarpX, kWarpMma = S::kWarpMma, kWarpDecode = S::kWarpDecode, kWarpOut = S::kWarpOut,
+                kWarpW = S::kWarpW, kThreads = S::kThreads;
+  extern __shared__ __align__(16) uint8_t table[];  // first, so that its address is a constant of the lookups
+  const uint32_t smem = (smem_addr(table) + (TABLE ? kTableBytes : 0) + 1023) & ~1023u;
+  uint8_t* smem_ptr = table + (smem - smem_addr(table));
   // ready: a stage's activations (one arrival and their bytes) and its decoded weights (4
   // warps); the first CTA of a pair also waits for its second's.  done: it is multiplied.
   __shared__ uint64_t ready[kRing], done[kRing], w_full[S::kWSlots], w_empty[S::kWSlots], acc_full[2], acc_empty[2];
@@ -180,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     }
     for (int i = 0; i < S::kWSlots; ++i) {
       mbar_init(&w_full[i], 1);
-      mbar_init(&w_empty[i], 8);
+      mbar_init(&w_empty[i], 4 * S::kGroups);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -189,6 +204,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kWarpMma) tmem_alloc_cg<CG>(&tmem_slot, 512);
+  const uint32_t lane4 = lane * 4;
+  if (TABLE && warp >= kWarpDecode && warp < kWarpOut) {  // a warp's 16 bytes, decoded by a lane each
+    const int b0 = (warp - kWarpDecode) * 16;
+    uint32_t h[4];
+    e2m1x8_decode<TYPE>(b0 + (lane & 15), h);
+#pragma unroll
+    for (int b = 0; b < 16; ++b)
+      *reinterpret_cast<uint32_t*>(table + (b0 + b) * 256 + lane4) = __shfl_sync(0xFFFFFFFFu, h[0], b);
+  }
   tc_fence_before_sync();
   __syncthreads();
   if (CG > 1) cluster_sync();  // the pair's barriers are ready before either arrives on them
@@ -222,8 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     failed = 1;
     return false;
   };
-  // one lane waits for its warp
-  const auto warp_ok = [&](auto&& waits) { return __shfl_sync(0xFFFFFFFFu, lane == 0 ? waits() : false, 0); };
+  // a warp waits as one
+  const auto warp_ok = [&](auto&& waits) { return __all_sync(0xFFFFFFFFu, waits()) != 0; };
 
   if (warp == kWarpX && lane == 0) {
     // ---- activations
@@ -337,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       if (ok && issuer) umma_commit_cg<CG>(&acc_full[acc]);
     }
   } else if (warp >= kWarpDecode && warp < kWarpOut) {
-    // ---- decoding: two groups of four warps, taking stages in turn
+    // ---- decoding
     const uint32_t group = (warp - kWarpDecode) >> 2, quad = warp & 3;
     const int tid = quad * 32 + lane;
     Ring<kRing> r;
@@ -350,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         const uint32_t at = smem + S::kW + w.slot * kSlotBytes, sc = smem + S::kS + w.slot * kSlotScales;
         const int n = stages_of(s);
         for (int j = 0; j < n; ++j, r.next()) {
-          if ((r.slot & 1) != group) continue;
+          if (r.slot % S::kGroups != group) continue;
           ok = warp_ok([&] { return wait(&done[r.slot], r.phase ^ 1, kSitePipeEmpty); });
           if (!ok) break;
           constexpr int kWords = mx4_block(FORMAT) / 8;  // words of a block
@@ -372,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 #pragma unroll
               for (int k = 0; k < kWords; ++k) {
                 uint32_t h[4];
-                decode_scaled<TYPE>(words[b * kWords + k], scale, h);
+                decode_scaled<TYPE, TABLE>(table, lane4, words[b * kWords + k], scale, h);
                 *reinterpret_cast<uint4*>(a + mn_offset(nl, half * 8 + b * kWords + k)) = make_uint4(h[0], h[1], h[2], h[3]);
               }
             }
@@ -394,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 const uint32_t scale = real ? scale_pair<FORMAT, TYPE>(four >> (8 * b) & 0xFF) : 0;
 #pragma unroll
                 for (int k = 0; k < kWords; ++k)
-                  decode_scaled<TYPE>(words[b * kWords + k], scale, *reinterpret_cast<uint32_t(*)[4]>(out + (b * kWords + k) * 4));
+                  decode_scaled<TYPE, TABLE>(table, lane4, words[b * kWords + k], scale, *reinterpret_cast<uint32_t(*)[4]>(out + (b * kWords + k) * 4));
               }
               tmem_st_x32(tmem + kATmem + r.slot * S::kACols + h * 32 + (quad << 21), out);
             }
@@ -521,10 +545,12 @@ size_t restaged_bytes(int type, int format, long long depth, long long batch) {
 
 struct Tiling {
   int nt, cg, splits;
+  bool table;
 };
 
-// Tokens of a tile, pairs and the split of the reduction.  A CTA's stages hold 128 tokens
-// (192 for dx, whose stages are half as deep), a pair's 256; half of that for two parts.
+// Tokens of a tile, pairs and the split of the reduction.  A pair's stages hold 256 tokens, a
+// CTA's 128 (192 for dx, whose stages are half as deep), or 64 beside the table; half of that
+// for two parts.
 Tiling plan(int features, int depth, int batch, int parts, bool grad) {
   const int slots = (depth + kSlotDepth - 1) / kSlotDepth;
   const int f_tiles = (features + kF - 1) / kF;
@@ -534,14 +560,15 @@ Tiling plan(int features, int depth, int batch, int parts, bool grad) {
   };
   if (batch > 128) {
     const int nt = even(256 / parts, 32);
-    if (static_cast<long long>(f_tiles + 1) / 2 * ((batch + nt - 1) / nt) >= kSms / 4) return {nt, 2, 1};
+    if (static_cast<long long>(f_tiles + 1) / 2 * ((batch + nt - 1) / nt) >= kSms / 4) return {nt, 2, 1, false};
   }
-  const int nt = even((grad ? 192 : 128) / parts, 16);
+  const bool table = batch <= 64 / parts;
+  const int nt = even(table ? 64 / parts : (grad ? 192 : 128) / parts, 16);
   const int t_tiles = (batch + nt - 1) / nt;
   int splits = 1;
   while (splits < 8 && static_cast<long long>(f_tiles) * t_tiles * splits * 2 <= kSms && slots >= 2 * splits * 2)
     splits *= 2;
-  return {nt, 1, splits};
+  return {nt, 1, splits, table};
 }
 
 cudaError_t map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* p, uint64_t cols, uint64_t rows, uint64_t pitch,
@@ -556,9 +583,9 @@ cudaError_t map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* p, ui
              : cudaErrorInvalidValue;
 }
 
-template <int FORMAT, int TYPE, bool GRAD, int CG>
+template <int FORMAT, int TYPE, bool GRAD, int CG, bool TABLE>
 cudaError_t launch_linear(const Call& c, const Tiling& tl, uint32_t* status, cudaStream_t stream) {
-  using S = Shape<GRAD>;
+  using S = Shape<GRAD, TABLE>;
   const int parts = split_parts(c.type, c.format) ? 2 : 1;
   const int pitch = (c.depth + 7) / 8 * 8;
   const void* x = c.x;
@@ -599,19 +626,21 @@ cudaError_t launch_linear(const Call& c, const Tiling& tl, uint32_t* status, cud
   q.out_type = c.type;
   const long long tiles = static_cast<long long>(q.f_tiles) * q.t_tiles;
   if (tiles > 0x7FFFFFFF / 8) return cudaErrorInvalidValue;
-  auto* kernel = linear_kernel<FORMAT, TYPE, GRAD, CG>;
+  auto* kernel = linear_kernel<FORMAT, TYPE, GRAD, CG, TABLE>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
   if (e != cudaSuccess) return e;
   const long long ctas = tiles * CG * tl.splits;
   const unsigned grid = static_cast<unsigned>(tl.splits > 1 || ctas < kSms ? ctas : kSms);
-  return launch_overlapped(kernel, grid, kThreads, S::kSmem, stream, CG * tl.splits, x_map, w_map, q);
+  return launch_overlapped(kernel, grid, S::kThreads, S::kSmem, stream, CG * tl.splits, x_map, w_map, q);
 }
 
 template <bool GRAD>
 cudaError_t run(const Call& c, uint32_t* status, cudaStream_t stream) {
   const Tiling tl = plan(c.features, c.depth, c.batch, split_parts(c.type, c.format) ? 2 : 1, GRAD);
-#define MX4_CASE(f, t) \
-  return tl.cg == 2 ? launch_linear<f, t, GRAD, 2>(c, tl, status, stream) : launch_linear<f, t, GRAD, 1>(c, tl, status, stream);
+#define MX4_CASE(f, t)                                                                     \
+  return tl.cg == 2   ? launch_linear<f, t, GRAD, 2, false>(c, tl, status, stream)         \
+         : tl.table   ? launch_linear<f, t, GRAD, 1, true>(c, tl, status, stream)          \
+                      : launch_linear<f, t, GRAD, 1, false>(c, tl, status, stream);
   if (c.format == kMxfp4) { MX4_CASE(kMxfp4, kBf16) }
   if (c.type == kF16) { MX4_CASE(kNvfp4, kF16) }
   MX4_CASE(kNvfp4, kBf16)
