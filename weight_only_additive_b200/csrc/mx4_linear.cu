@@ -49,7 +49,10 @@ struct Shape {
   static constexpr int kW = kX + kXBytes;
   static constexpr int kS = kW + kWSlots * kSlotBytes;
   static constexpr size_t kSmem = (TABLE ? kTableBytes : 0) + kS + kWSlots * kSlotScales + 1024;
-  static_assert(kRing % kGroups == 0, "");
+  // With more groups than stages in a slot, sets of groups take slots in turn.
+  static constexpr int kSets = kGroups > kSlotStages ? kGroups / kSlotStages : 1;
+  static constexpr int kSetGroups = kGroups / kSets;
+  static_assert(kRing % kGroups == 0 && kSlotStages % kSetGroups == 0, "");
 };
 constexpr uint32_t kATmem = 256;  // first TMEM column of the decoded stages
 
@@ -149,14 +152,15 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
-      "tcgen05.wait::st.sync.aligned;"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
       ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
         "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
         "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
     }
     for (int i = 0; i < S::kWSlots; ++i) {
       mbar_init(&w_full[i], 1);
-      mbar_init(&w_empty[i], 4 * S::kGroups);
+      mbar_init(&w_empty[i], 4 * S::kSetGroups);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -234,7 +238,6 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
   const uint32_t x_part = x_box * (S::kDepth / 64), x_stage = x_part * p.parts;
   const auto features_at = [&](int t) { return (t / p.t_tiles) * kF * CG + (CG > 1 ? rank * kF : 0); };
   const auto tokens_at = [&](int t) { return (t % p.t_tiles) * p.nt; };
-  const auto stages_of = [&](int s) { return min(S::kSlotStages, (p.depth - s * kSlotDepth + S::kDepth - 1) / S::kDepth); };
   // a wait that gives up makes every later one of this CTA that is not over end soon
   const auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
     if (mbar_wait_sleeping<false>(bar, parity, p.status, site, &failed)) return true;
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
     for (int t = first; t < total && ok; t += step) {
       const int row = tokens_at(t) + (CG > 1 ? rank * (p.nt / CG) : 0);
       for (int s = s0; s < s1 && ok; ++s)
-        for (int j = 0, n = stages_of(s); j < n; ++j, r.next(), ++issued) {
+        for (int j = 0; j < S::kSlotStages; ++j, r.next(), ++issued) {
           ok = wait(&done[r.slot], r.phase ^ 1, kSitePipeEmpty);
           if (!ok) break;
           uint32_t at = smem + S::kX + r.slot * x_stage;
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
     bool ok = true;
     for (int t = first; t < total && ok; t += step)
       for (int s = s0; s < s1 && ok; ++s)
-        for (int j = 0, n = stages_of(s); j < n && ok; ++j, r.next()) {
+        for (int j = 0; j < S::kSlotStages && ok; ++j, r.next()) {
           ok = warp_ok([&] { return wait(&ready[r.slot], r.phase, kSitePipeFull); });
           if (ok && lane == 0) mbar_arrive_leader(&ready[r.slot]);
         }
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
       const uint32_t d = tmem + acc * acc_cols;
       uint32_t go = 0;
       for (int s = s0; s < s1 && ok; ++s)
-        for (int j = 0, n = stages_of(s); j < n; ++j, r.next()) {
+        for (int j = 0; j < S::kSlotStages; ++j, r.next()) {
           ok = wait_pair(&ready[r.slot], r.phase, kSitePipeFull);
           if (!ok) break;
           tc_fence_after_sync();
@@ -363,25 +366,25 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
   } else if (warp >= kWarpDecode && warp < kWarpOut) {
     // ---- decoding
     const uint32_t group = (warp - kWarpDecode) >> 2, quad = warp & 3;
+    const uint32_t set = group / S::kSetGroups, j0 = group % S::kSetGroups;
     const int tid = quad * 32 + lane;
-    Ring<kRing> r;
     Ring<S::kWSlots> w;
+    uint32_t seq = 0;  // slots so far
     bool ok = true;
     for (int t = first; t < total && ok; t += step)
-      for (int s = s0; s < s1 && ok; ++s, w.next()) {
+      for (int s = s0; s < s1 && ok; ++s, ++seq, w.next()) {
+        if (S::kSets > 1 && seq % S::kSets != set) continue;
         ok = warp_ok([&] { return wait(&w_full[w.slot], w.phase, kSitePipeCodes); });
         if (!ok) break;
         const uint32_t at = smem + S::kW + w.slot * kSlotBytes, sc = smem + S::kS + w.slot * kSlotScales;
-        const int n = stages_of(s);
-        for (int j = 0; j < n; ++j, r.next()) {
-          if (r.slot % S::kGroups != group) continue;
-          ok = warp_ok([&] { return wait(&done[r.slot], r.phase ^ 1, kSitePipeEmpty); });
-          if (!ok) break;
+#pragma unroll 1
+        for (uint32_t j = j0; j < S::kSlotStages; j += S::kSetGroups) {
+          const uint32_t stage = (seq * S::kSlotStages + j) % kRing, phase = (seq * S::kSlotStages + j) / kRing & 1;
           constexpr int kWords = mx4_block(FORMAT) / 8;  // words of a block
           if constexpr (GRAD) {
             // weight row nl of the stage, 64 of its 128 features: eight lanes of a phase
             // have eight rows, so their 16-byte stores hit all banks
-            const int nl = tid & 63, half = tid >> 6, row = j * S::kDepth + nl;
+            const int nl = tid & 63, half = tid >> 6, row = static_cast<int>(j) * S::kDepth + nl;
             const uint32_t base = at + row * 64, turn = (row >> 1) & 3;
             const uint4 w0 = lds128(base + (((2 * half) ^ turn) << 4)), w1 = lds128(base + (((2 * half + 1) ^ turn) << 4));
             const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
@@ -389,7 +392,9 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
             uint32_t four = lds32(sc + (row >> 7) * (kSlotScales / 2) + chunk * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4);
             if (FORMAT == kMxfp4) four >>= half * 16;
             const bool real = s * kSlotDepth + row < p.depth;  // scales of rows past the end may be anything
-            uint8_t* a = smem_ptr + r.slot * S::kABytes;
+            uint8_t* a = smem_ptr + stage * S::kABytes;
+            ok = warp_ok([&] { return wait(&done[stage], phase ^ 1, kSitePipeEmpty); });
+            if (!ok) break;
 #pragma unroll
             for (int b = 0; b < 8 / kWords; ++b) {
               const uint32_t scale = real ? scale_pair<FORMAT, TYPE>(four >> (8 * b) & 0xFF) : 0;
@@ -404,13 +409,23 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
           } else {
             // lane = feature: 64 values of its row at a time
             const uint32_t base = at + tid * 128;
+            uint4 words[S::kDepth / 64][2];
+            uint32_t fours[S::kDepth / 64];
 #pragma unroll
             for (int h = 0; h < S::kDepth / 64; ++h) {
               const int c = j * (S::kDepth / 64) + h;  // 64 values: 32 bytes, a tile of NVFP4 scales, half an MXFP4 one
-              const uint4 w0 = lds128(base + (((2 * c) ^ (tid & 7)) << 4)), w1 = lds128(base + (((2 * c + 1) ^ (tid & 7)) << 4));
-              const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-              uint32_t four = lds32(sc + (FORMAT == kMxfp4 ? c >> 1 : c) * 512 + lane * 16 + quad * 4);
-              if (FORMAT == kMxfp4) four >>= (c & 1) * 16;
+              words[h][0] = lds128(base + (((2 * c) ^ (tid & 7)) << 4));
+              words[h][1] = lds128(base + (((2 * c + 1) ^ (tid & 7)) << 4));
+              fours[h] = lds32(sc + (FORMAT == kMxfp4 ? c >> 1 : c) * 512 + lane * 16 + quad * 4);
+            }
+            ok = warp_ok([&] { return wait(&done[stage], phase ^ 1, kSitePipeEmpty); });
+            if (!ok) break;
+#pragma unroll
+            for (int h = 0; h < S::kDepth / 64; ++h) {
+              const int c = j * (S::kDepth / 64) + h;
+              const uint32_t word[8] = {words[h][0].x, words[h][0].y, words[h][0].z, words[h][0].w,
+                                        words[h][1].x, words[h][1].y, words[h][1].z, words[h][1].w};
+              const uint32_t four = FORMAT == kMxfp4 ? fours[h] >> ((c & 1) * 16) : fours[h];
               const bool real = s * kSlotDepth + c * 64 < p.depth;  // there may be no scales there
               uint32_t out[32];
 #pragma unroll
@@ -418,14 +433,16 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
                 const uint32_t scale = real ? scale_pair<FORMAT, TYPE>(four >> (8 * b) & 0xFF) : 0;
 #pragma unroll
                 for (int k = 0; k < kWords; ++k)
-                  decode_scaled<TYPE, TABLE>(table, lane4, words[b * kWords + k], scale, *reinterpret_cast<uint32_t(*)[4]>(out + (b * kWords + k) * 4));
+                  decode_scaled<TYPE, TABLE>(table, lane4, word[b * kWords + k], scale,
+                                             *reinterpret_cast<uint32_t(*)[4]>(out + (b * kWords + k) * 4));
               }
-              tmem_st_x32(tmem + kATmem + r.slot * S::kACols + h * 32 + (quad << 21), out);
+              tmem_st_x32(tmem + kATmem + stage * S::kACols + h * 32 + (quad << 21), out);
             }
+            tmem_st_wait();
             tc_fence_before_sync();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ready[r.slot]);
+          if (lane == 0) mbar_arrive(&ready[stage]);
         }
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&w_empty[w.slot]);
