@@ -65,16 +65,23 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Eight codes as four pairs, in order, times `scale` (SCALED); `lane4`: 4 * lane.
-template <int TYPE, bool SCALED>
+// Eight codes as four pairs, in order, times `scale` (SCALED); `lane4`: 4 * lane.  LOOKUP: by
+// the table, else by logic operations.
+template <int TYPE, bool SCALED, bool LOOKUP>
 __device__ __forceinline__ void decode_pairs(const uint8_t* table, uint32_t lane4, uint32_t w, uint32_t scale,
                                              uint32_t (&h)[4]) {
+  if constexpr (LOOKUP) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(table + prmt(w, lane4, 0x5504 | j << 4));
-    if constexpr (!SCALED) h[j] = v;
-    else if constexpr (TYPE == kF16) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[j]) : "r"(v), "r"(scale));
-    else asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(h[j]) : "r"(v), "r"(scale));
+    for (int j = 0; j < 4; ++j) h[j] = *reinterpret_cast<const uint32_t*>(table + prmt(w, lane4, 0x5504 | j << 4));
+  } else {
+    e2m1x8_decode<TYPE>(w, h);
+  }
+  if constexpr (SCALED) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (TYPE == kF16) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[j]) : "r"(h[j]), "r"(scale));
+      else asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(h[j]) : "r"(h[j]), "r"(scale));
+    }
   }
 }
 
@@ -174,24 +181,26 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
     // what a lane holds of x in a step: its 32 values of a token, or half of them or none
     uint4 x[kN][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[0][i] = make_uint4(0, 0, 0, 0);
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[n][i] = make_uint4(0, 0, 0, 0);
+    const uint4* x_from[kN];  // the lane's values in stage 0; a token past the last reads the first
+    bool x_real[kN];
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const int token = kOne ? 0 : n * 8 + g;
+      x_real[n] = kOne ? g >> 1 == t : token < p.batch;
+      x_from[n] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) +
+                                                 static_cast<size_t>(x_real[n] ? token : 0) * p.K + (kw * 4 + t) * 32);
+    }
     const auto load_x = [&](int s) {
-      const int c = s * (kStage / 32) + kw * 4 + t;
-      const uint16_t* from_x = static_cast<const uint16_t*>(p.x) + c * 32;
-      if constexpr (kOne) {
-        const uint4* at = reinterpret_cast<const uint4*>(from_x);
-        if (g >> 1 == t) {
+      const bool in = s * (kStage / 32) + kw * 4 + t < chunks;
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        if (x_real[n]) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (i >> 1 == (g & 1)) x[0][i] = c < chunks ? ldg_nc_v4(at + i) : make_uint4(0, 0, 0, 0);
-        }
-      } else {
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          const int token = n * 8 + g;
-          const uint4* at = reinterpret_cast<const uint4*>(from_x + static_cast<size_t>(token) * p.K);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[n][i] = c < chunks && token < p.batch ? ldg_nc_v4(at + i) : make_uint4(0, 0, 0, 0);
+            if (!kOne || i >> 1 == (g & 1)) x[n][i] = in ? ldg_nc_v4(x_from[n] + s * (kStage / 8) + i) : make_uint4(0, 0, 0, 0);
         }
       }
     };
@@ -237,8 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
 #pragma unroll
               for (int m = 0; m < 2; ++m) {
                 uint32_t up[4], down[4];
-                decode_pairs<TYPE, false>(table, lane4, w[2 * m][i], 0, up);
-                decode_pairs<TYPE, false>(table, lane4, w[2 * m + 1][i], 0, down);
+                decode_pairs<TYPE, false, true>(table, lane4, w[2 * m][i], 0, up);
+                decode_pairs<TYPE, false, true>(table, lane4, w[2 * m + 1][i], 0, down);
                 mma16816<TYPE>(sum[m][0], up[0], down[0], up[1], down[1], x[0][i].x, x[0][i].y);
                 mma16816<TYPE>(sum[m][1], up[2], down[2], up[3], down[3], x[0][i].z, x[0][i].w);
               }
@@ -271,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
 #pragma unroll
               for (int m = 0; m < 2; ++m) {
                 uint32_t up[4], down[4];
-                decode_pairs<TYPE, true>(table, lane4, w[2 * m][i], scale[2 * m][i >> 1], up);
-                decode_pairs<TYPE, true>(table, lane4, w[2 * m + 1][i], scale[2 * m + 1][i >> 1], down);
+                decode_pairs<TYPE, true, true>(table, lane4, w[2 * m][i], scale[2 * m][i >> 1], up);
+                decode_pairs<TYPE, true, false>(table, lane4, w[2 * m + 1][i], scale[2 * m + 1][i >> 1], down);
 #pragma unroll
                 for (int n = 0; n < kN; ++n) {
                   mma16816<TYPE>(acc[m][n], up[0], down[0], up[1], down[1], b[n][0], b[n][1]);

@@ -576,7 +576,15 @@ Tiling plan(int features, int depth, int batch, int parts, bool grad) {
     return ((batch + t_tiles - 1) / t_tiles + unit - 1) / unit * unit;
   };
   if (batch > 128) {
-    const int nt = even(256 / parts, 32);
+    // rounds of pairs over the SMs times a stage's time: its MMAs, or the decoding where the
+    // tile is narrower than that takes, and a little for every stage
+    int nt = 0;
+    long long best = 0;
+    for (int n = 256 / parts; n >= 64; n -= 16) {
+      const long long tiles = static_cast<long long>(f_tiles + 1) / 2 * ((batch + n - 1) / n);
+      const long long cost = (tiles + kSms / 2 - 1) / (kSms / 2) * ((n * parts > 208 ? n * parts : 208) + 16);
+      if (!best || cost < best) best = cost, nt = n;
+    }
     if (static_cast<long long>(f_tiles + 1) / 2 * ((batch + nt - 1) / nt) >= kSms / 4) return {nt, 2, 1, false};
   }
   const bool table = batch <= 64 / parts;
