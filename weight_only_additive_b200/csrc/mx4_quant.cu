@@ -1,7 +1,7 @@
 // Quantisation to and dequantisation from microscaled 4-bit floating point.
 //
-// Both are one pass bound by HBM: a thread takes 16 (quantise) or 32 (dequantise)
-// consecutive values of a row.
+// Both are one pass bound by HBM: a thread takes 32 consecutive values of a
+// row at a time.
 #include "mx4_device.cuh"
 
 namespace aqlm {
@@ -86,7 +86,6 @@ __device__ __forceinline__ uint32_t exact_e2m1(float x, double unit) {
 }
 
 // `codes` of the eight values at x, those whose nibble is set in `doubt` decided exactly.
-// Rare, so out of the way of the registers and instructions of the common path.
 template <int TYPE>
 __device__ __noinline__ uint32_t settle(const void* x, uint32_t codes, uint32_t doubt, float s, float gamma) {
   const double unit = static_cast<double>(s) * static_cast<double>(gamma);
@@ -99,11 +98,27 @@ __device__ __noinline__ uint32_t settle(const void* x, uint32_t codes, uint32_t 
   return codes;
 }
 
-// e4m3 of the exact quotient amax / (6 gamma) where fp32 leaves it open.  The 64-bit quotient
-// is within 2^-52 of it; one that is not a tie stays 2^-33 away from every tie (its terms have
-// 24 and 27 bits), so what lies within 2^-40 of an fp32 value is that value, and anything else
-// goes to the odd fp32 neighbour: the conversion then rounds it as it would the quotient.
-__device__ __noinline__ uint32_t settle_scale(float amax, float gamma) {
+// The sign of x - b c for a product within a few units in the last place of x, exact: the
+// difference to the rounded product and that product's error have few bits each.  `c_low` is
+// what c lacks.
+__device__ __forceinline__ float beyond(float x, float b, float c, float c_low) {
+  const float p = b * c;
+  return (x - p) - fmaf(b, c_low, fmaf(b, c, -p));
+}
+
+// e4m3 of amax / (6 gamma) that lies next to the border between the neighbours `low` and
+// low + 1: by the exact comparison of amax with it, ties to the even code.
+__device__ __forceinline__ uint32_t settle_scale(float amax, float gamma, uint32_t low) {
+  const float border = 3.0f * (mx4_scale_value<kNvfp4>(low) + mx4_scale_value<kNvfp4>(low + 1));  // 6 bits
+  const float d = beyond(amax, border, gamma, 0.0f);
+  return low + (d > 0.0f || (d == 0.0f && (low & 1)) ? 1 : 0);
+}
+
+// The same for a gamma that fp32 quotients do not hold.  The 64-bit quotient is within 2^-52 of
+// the exact one, which stays 2^-33 away from every tie unless it is one (its terms have 24 and
+// 27 bits), so what lies within 2^-40 of an fp32 value is that value, and anything else goes to
+// the odd fp32 neighbour: the conversion then rounds it as it would the quotient.
+__device__ __noinline__ uint32_t scale_of_extreme(float amax, float gamma) {
   const double v = fmin(static_cast<double>(amax) / (6.0 * static_cast<double>(gamma)), 1024.0);
   const float f = __double2float_rn(v);
   const double r = v - static_cast<double>(f);
@@ -115,7 +130,37 @@ __device__ __noinline__ uint32_t settle_scale(float amax, float gamma) {
   return to_e4m3(__uint_as_float(bits));
 }
 
-// A thread's 16 values and the largest of their magnitudes.
+// Which way the 16-bit values go that lie next to a border of a block.  The borders are 1, 3, 5
+// and 7 units times powers of two, and at most one value of the type is that close to each: all
+// ones for up.  A value on the border goes to the even code: up at 3 and 7 units.
+struct Ways {
+  uint32_t up[4];
+  template <int TYPE>
+  __device__ __forceinline__ void find(float unit, float unit_low) {
+    constexpr int kDrop = TYPE == kBf16 ? 16 : 13;  // fp32 bits below the type's last
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float m = 2 * i + 1;
+      const float x = __uint_as_float((__float_as_uint(m * unit) + (1u << (kDrop - 1))) & ~((1u << kDrop) - 1));
+      const float d = beyond(x, m, unit, unit_low);
+      up[i] = d > 0.0f || (d == 0.0f && (i & 1)) ? 0xFFFFFFFFu : 0;
+    }
+  }
+  // eight codes of which those that differ are next to a border, `low` below it
+  __device__ __forceinline__ uint32_t choose(uint32_t low, uint32_t high) const {
+    const uint32_t d = low ^ high;
+    const uint32_t differ = (d | d >> 1 | d >> 2) & 0x11111111u, odd = low, above = low >> 1 | low >> 2;
+    // code 0: 1 unit; 1: 3; 2, 4, 6: 5; 3, 5: 7
+    const uint32_t way = (odd & ((above & up[3]) | (~above & up[1]))) | (~odd & ((above & up[2]) | (~above & up[0])));
+    return low + (way & differ);
+  }
+};
+
+// CTAs of the quantisation on an SM, by the registers that a thread's values take.
+template <int TYPE>
+constexpr int kQuantizeCtas = TYPE == kF32 ? 3 : 4;
+
+// 16 values and the largest of their magnitudes.
 template <int TYPE>
 struct Values {
   uint32_t raw[TYPE == kF32 ? 16 : 8];
@@ -161,12 +206,12 @@ struct Values {
   }
 };
 
-// Rows of `units` 16-value pieces, the last ones past K filling the row's last scale tile.
+// Rows of `units` pieces of 32 values (one MXFP4 or two NVFP4 blocks), the last ones past K
+// filling the row's last scale tile.
 template <int FORMAT, int TYPE>
-__global__ void __launch_bounds__(kThreads, TYPE == kF32 ? 4 : 5) quantize_kernel(const void* __restrict__ x, uint8_t* __restrict__ packed,
-                                                            uint8_t* __restrict__ scales,
-                                                            const float* __restrict__ tensor_scale, int rows,
-                                                            int units, int K, int tiles, bool wide) {
+__global__ void __launch_bounds__(kThreads, kQuantizeCtas<TYPE>) quantize_kernel(
+    const void* __restrict__ x, uint8_t* __restrict__ packed, uint8_t* __restrict__ scales,
+    const float* __restrict__ tensor_scale, int rows, int units, int K, int tiles, bool wide) {
   grid_dependency_wait();
   grid_dependents_launch();
   const float gamma = FORMAT == kNvfp4 && tensor_scale ? *tensor_scale : 1.0f;
@@ -174,89 +219,126 @@ __global__ void __launch_bounds__(kThreads, TYPE == kF32 ? 4 : 5) quantize_kerne
   // 1 / (6 gamma), or 0 where fp32 cannot hold it well
   const float inv6 = gamma > 0x1p-120f && gamma < 0x1p100f ? 1.0f / (6.0f * gamma) : 0.0f;
   const int lane = threadIdx.x & 31;
-  // the next piece is loaded before this one is converted; the lanes of a warp, whose pieces
-  // are neighbours, go on together while any has one
+  // 16-bit values are loaded a piece ahead; the lanes of a warp, whose pieces are neighbours,
+  // go on together while any has one
+  constexpr bool kAhead = TYPE != kF32;
   Walk way(static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x, static_cast<long long>(gridDim.x) * kThreads, units);
-  const auto fetch = [&](Values<TYPE>& v) {
-    if (way.row < rows && way.u * 16 < K) v.load(x, static_cast<size_t>(way.row) * K + static_cast<size_t>(way.u) * 16, wide);
-    else v.zero();
+  const auto fetch = [&](Values<TYPE>(&v)[2]) {
+    if (way.row < rows && way.u * 32 < K) {
+      const size_t at = static_cast<size_t>(way.row) * K + static_cast<size_t>(way.u) * 32;
+      v[0].load(x, at, wide);
+      v[1].load(x, at + 16, wide);
+    } else {
+      v[0].zero();
+      v[1].zero();
+    }
   };
-  Values<TYPE> ahead;
-  fetch(ahead);
+  Values<TYPE> ahead[2];
+  if (kAhead) fetch(ahead);
   while (__any_sync(0xFFFFFFFFu, way.row < rows)) {
-    const Values<TYPE> v = ahead;
+    if (!kAhead) fetch(ahead);
+    const Values<TYPE> v[2] = {ahead[0], ahead[1]};
     const int row = way.row, u = way.u;
-    const bool inside = row < rows && u * 16 < K;
-    const size_t at = static_cast<size_t>(row) * K + static_cast<size_t>(u) * 16;
+    const bool inside = row < rows && u * 32 < K;
+    const size_t at = static_cast<size_t>(row) * K + static_cast<size_t>(u) * 32;
     way.next();
-    fetch(ahead);
-    uint32_t top = v.amax_bits();
-    if (FORMAT == kMxfp4) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    const bool bad = top >= (TYPE == kF32 ? 0x7F800000u : TYPE == kBf16 ? 0x7F80u : 0x7C00u);
-    const float amax = bad ? 0.0f : Values<TYPE>::as_float(top);
+    if (kAhead) fetch(ahead);
 
-    uint32_t code;    // the block's scale
-    uint2 q = {0, 0};  // 16 e2m1 codes
+    uint32_t code = 0;     // the scales, one byte or two
+    uint32_t q[4] = {};    // 32 e2m1 codes
     float f[8];
+    constexpr uint32_t kInfinity = TYPE == kF32 ? 0x7F800000u : TYPE == kBf16 ? 0x7F80u : 0x7C00u;
     if constexpr (FORMAT == kMxfp4) {
-      const uint32_t e = __float_as_uint(amax) >> 23;
-      code = e > 2 ? e - 2 : 0;
-      const float inv = __uint_as_float((254u - code) << 23);  // 2^(127 - code), exact
-      if (!bad) {
+      const uint32_t top = max(v[0].amax_bits(), v[1].amax_bits());
+      if (top < kInfinity) {
+        const uint32_t e = __float_as_uint(Values<TYPE>::as_float(top)) >> 23;
+        code = e > 2 ? e - 2 : 0;
+        const float inv = __uint_as_float((254u - code) << 23);  // 2^(127 - code), exact
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          v.eight(h, f);
+        for (int h = 0; h < 4; ++h) {
+          v[h >> 1].eight(h & 1, f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] *= inv;
-          (h ? q.y : q.x) = to_e2m1x8(f);
+          q[h] = to_e2m1x8(f);
         }
       } else {
         code = 0xFF;
       }
     } else {
-      // fp32 quotients are within 2^-21; where that much to either side gives two codes, or
-      // fp32 cannot hold them, the exact comparison decides
-      const float v6 = amax * inv6;
-      uint32_t both;
-      asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}"
-          : "=r"(both) : "f"(v6 * (1.0f + 0x1p-20f)), "f"(v6 * (1.0f - 0x1p-20f)));
-      code = both & 0xFF;
-      if ((both >> 8 != code || inv6 == 0.0f) && gamma > 0.0f) code = settle_scale(amax, gamma);
-      if (bad || gamma_bad) {
-        code = 0x7F;
-      } else if (code != 0) {
-        const float s = mx4_scale_value<kNvfp4>(code);
+      // Scales: fp32 quotients are within 2^-21; where that much to either side gives two
+      // codes, or fp32 cannot hold them, the exact comparison decides.
+      bool bad[2];
+      float amax[2];
+      uint32_t c[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t top = v[b].amax_bits();
+        bad[b] = top >= kInfinity || gamma_bad;
+        amax[b] = bad[b] ? 0.0f : Values<TYPE>::as_float(top);
+        const float v6 = amax[b] * inv6;
+        uint32_t both;
+        asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}"
+            : "=r"(both) : "f"(v6 * (1.0f + 0x1p-20f)), "f"(v6 * (1.0f - 0x1p-20f)));
+        c[b] = both & 0xFF;
+        if (both >> 8 != c[b]) c[b] = settle_scale(amax[b], gamma, c[b]);
+        if (inv6 == 0.0f && gamma > 0.0f) c[b] = scale_of_extreme(amax[b], gamma);
+      }
+      // Values, likewise.
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const float s = mx4_scale_value<kNvfp4>(c[b]);
         const float unit = s * gamma;
-        const bool plain = unit > 0x1p-100f && unit < 0x1p100f;
-        const float inv = __fdividef(1.0f, unit);
+        const bool plain = unit > 0x1p-100f && unit < 0x1p100f, zero = bad[b] || c[b] == 0;
+        const float inv = plain && !zero ? __fdividef(1.0f, unit) : 0.0f;
         const float below = inv * (1.0f - 0x1p-20f), above = inv * (1.0f + 0x1p-20f);
+        uint32_t low[2], high[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float g[8];
-          v.eight(h, f);
+          v[b].eight(h, f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) g[i] = f[i] * above;
-          const uint32_t hi = to_e2m1x8(g);
+          high[h] = to_e2m1x8(g);
 #pragma unroll
           for (int i = 0; i < 8; ++i) g[i] = f[i] * below;
-          uint32_t lo = to_e2m1x8(g);
-          const uint32_t doubt = plain ? hi ^ lo : 0xFFFFFFFFu;
-          if (doubt && inside)
-            lo = settle<TYPE>(static_cast<const uint8_t*>(x) + (at + 8 * h) * (TYPE == kF32 ? 4 : 2), lo, doubt, s, gamma);
-          (h ? q.y : q.x) = lo;
+          low[h] = to_e2m1x8(g);
         }
+        if (TYPE != kF32 && low[0] == high[0] && low[1] == high[1] && (plain || zero)) {
+          // nothing next to a border
+        } else if (TYPE != kF32 && plain) {
+          Ways ways;
+          ways.find<TYPE>(unit, fmaf(s, gamma, -unit));
+          low[0] = ways.choose(low[0], high[0]);
+          low[1] = ways.choose(low[1], high[1]);
+        } else if (!zero && inside) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t doubt = plain ? low[h] ^ high[h] : 0xFFFFFFFFu;
+            if (doubt) low[h] = settle<TYPE>(static_cast<const uint8_t*>(x) + (at + 16 * b + 8 * h) * (TYPE == kF32 ? 4 : 2),
+                                             low[h], doubt, s, gamma);
+          }
+        }
+        q[2 * b] = zero ? 0 : low[0];
+        q[2 * b + 1] = zero ? 0 : low[1];
+        code |= (bad[b] ? 0x7Fu : c[b]) << (8 * b);
       }
     }
-    if (inside) *reinterpret_cast<uint2*>(packed + at / 2) = q;
+    if (inside) *reinterpret_cast<uint4*>(packed + at / 2) = make_uint4(q[0], q[1], q[2], q[3]);
 
     // the four scales of a tile's row together
     if (!inside) code = 0;
-    constexpr int kPer = FORMAT == kMxfp4 ? 2 : 1;  // threads per block
-    uint32_t four = code << (8 * ((lane / kPer) & 3));
-    four |= __shfl_xor_sync(0xFFFFFFFFu, four, kPer);
-    four |= __shfl_xor_sync(0xFFFFFFFFu, four, 2 * kPer);
-    if (row < rows && (lane & (4 * kPer - 1)) == 0)
-      *reinterpret_cast<uint32_t*>(scales + mx4_scale_at(row, u / kPer, tiles)) = four;
+    uint32_t four;
+    if constexpr (FORMAT == kMxfp4) {
+      four = code << (8 * (lane & 3));
+      four |= __shfl_xor_sync(0xFFFFFFFFu, four, 1);
+      four |= __shfl_xor_sync(0xFFFFFFFFu, four, 2);
+    } else {
+      four = code << (16 * (lane & 1));
+      four |= __shfl_xor_sync(0xFFFFFFFFu, four, 1);
+    }
+    constexpr int kPer = FORMAT == kMxfp4 ? 4 : 2;  // threads of a tile's row
+    if (row < rows && lane % kPer == 0)
+      *reinterpret_cast<uint32_t*>(scales + mx4_scale_at(row, u * (4 / kPer), tiles)) = four;
   }
 }
 
@@ -327,9 +409,9 @@ template <int FORMAT, int TYPE>
 cudaError_t quantize_as(const void* x, uint8_t* packed, uint8_t* scales, const float* tensor_scale, int rows, int K,
                         cudaStream_t stream) {
   const int tiles = mx4_scale_tiles(K, FORMAT);
-  const int units = tiles * 4 * mx4_block(FORMAT) / 16;
+  const int units = tiles * 4 * mx4_block(FORMAT) / 32;
   const long long total = static_cast<long long>(rows) * units;
-  return launch_overlapped(quantize_kernel<FORMAT, TYPE>, blocks_for(total, TYPE == kF32 ? 4 : 5), kThreads, 0, stream, 1,
+  return launch_overlapped(quantize_kernel<FORMAT, TYPE>, blocks_for(total, kQuantizeCtas<TYPE>), kThreads, 0, stream, 1,
                            x, packed, scales, tensor_scale, rows, units, K, tiles, aligned32(x));
 }
 
