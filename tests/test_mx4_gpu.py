@@ -125,6 +125,20 @@ def test_quantize_mxfp4_at_the_borders(dev, dtype):
     check_quantize(torch.stack(blocks), MX, None, dev)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("top", [5.03125, 3.0, 7.0, 1.3125, 6.5625, 10.5, 441.0])
+def test_quantize_with_the_usual_tensor_scale(dev, dtype, top):
+    """tensor_scale = max / 2688, rounded to fp32: quotients of few bits, so that many values
+    lie on a border but for that rounding."""
+    g = gen(int(top * 32))
+    x = (torch.randn((64, 2048), generator=g) * top / 3).clamp(-top, top)
+    x = (x * 8).round() / 8 if top < 20 else x.round()
+    x[7, 9] = top
+    x = x.to(dtype)
+    check_quantize(x, NV, float(torch.tensor(top) / 2688), dev)
+    check_quantize(x, NV, 1.0, dev)
+
+
 @pytest.mark.parametrize("fmt", [MX, NV])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_quantize_special_values(dev, fmt, dtype):
@@ -313,6 +327,24 @@ def test_products_over_many_features_exact(dev, fmt, dtype, batch):
     status_ok()
 
 
+@pytest.mark.parametrize("seed", range(48))
+def test_products_of_any_size_exact(dev, seed):
+    import random
+    r = random.Random(seed)
+    log = lambda lo, hi: int(lo * (hi / lo) ** r.random())  # noqa: E731
+    fmt, dtype = r.choice((MX, NV)), r.choice(TYPES[:2])
+    batch, N, K = log(1, 700), log(1, 3000), 32 * log(1, 100)
+    w, W = whole(N, K, fmt, seed, dev)
+    x = torch.randint(-3, 4, (batch, K), generator=gen(seed, 5)).to(dtype)
+    what = (fmt, dtype, batch, N, K)
+    assert torch.equal(mx4.matmul(x.to(dev), w).cpu(), once(x.double() @ W.T, dtype)), what
+    q, X = whole(batch, K, fmt, seed + 1, dev)
+    assert torch.equal(mx4.matmul(q, w, out_dtype=dtype).cpu(), once(X @ W.T, dtype)), what
+    dy = torch.randint(-2, 3, (batch, N), generator=gen(seed, 6)).to(dtype)
+    assert torch.equal(mx4.input_grad(dy.to(dev), w).cpu(), once(dy.double() @ W, dtype)), what
+    status_ok()
+
+
 @pytest.mark.parametrize("fmt", [MX, NV])
 @pytest.mark.parametrize("dtype", TYPES[:2])
 @pytest.mark.parametrize("batch,N,K", [(1, 1024, 4096), (5, 500, 2080), (40, 384, 4096), (300, 700, 1024)])
@@ -488,8 +520,14 @@ def test_offsets_past_32_bits(dev):
         assert same(y[-3:].cpu(), ref.values(codes, bytes_, fmt).to(torch.bfloat16))
         assert not y[:1000].any()
         del y
-        one = torch.ones((2, K), dtype=torch.bfloat16, device=dev)
-        got = mx4.matmul(one, q).cpu()
         W = ref.values(codes, bytes_, fmt)
-        close(got[:, -3:], torch.ones((2, K), dtype=torch.float64) @ W.T, W.abs().sum(1).expand(2, 3), K, torch.bfloat16)
+        for batch in (2, 20):  # the kernels for a few tokens and for more
+            one = torch.ones((batch, K), dtype=torch.bfloat16, device=dev)
+            want, mags = torch.ones((batch, K), dtype=torch.float64) @ W.T, W.abs().sum(1).expand(batch, 3)
+            close(mx4.matmul(one, q).cpu()[:, -3:], want, mags, K, torch.bfloat16)
+        y = mx4.matmul(mx4.quantize(one, fmt), q, out_dtype=torch.bfloat16)
+        close(y.cpu()[:, -3:], want, mags, K, torch.bfloat16)
+        dy = torch.zeros((5, rows), dtype=torch.bfloat16, device=dev)
+        dy[:, -3:] = 1
+        close(mx4.input_grad(dy, q).cpu(), W.sum(0).expand(5, K), W.abs().sum(0).expand(5, K), 3, torch.bfloat16)
         del q
