@@ -26,7 +26,7 @@
 namespace aqlm {
 namespace {
 
-constexpr int kSet = 8, kWarps = 2 * kSet, kConsumers = kWarps * 32, kThreads = kConsumers + 32;
+constexpr int kSet = 8, kWarps = 2 * kSet, kThreads = (kWarps + 2) * 32;  // and a warp that loads, one that adds
 constexpr int kRows = 32, kStage = 1024, kBox = 256, kStep = 128;
 constexpr int kStageBytes = kRows * kStage / 2;
 constexpr int kTableBytes = 65536;
@@ -36,7 +36,11 @@ template <int FORMAT, int NB>
 struct Shape {
   static constexpr int kTiles = kStage / (4 * mx4_block(FORMAT));  // scale tiles of a stage
   static constexpr int kSlot = kStageBytes + kTiles * 512;
-  static constexpr int kPart = 2 * kWarps * kRows * (NB ? NB : 1) * 8 * 4;  // two sets of the warps' sums
+  static constexpr int kTokens = NB ? NB * 8 : 1;
+  static constexpr int kPitch = 36;  // floats of a token's 32 sums: a warp's writes hit all banks
+  static constexpr int kSums = kTokens * kPitch;
+  static constexpr int kSets = NB > 1 ? 1 : 2;
+  static constexpr int kPart = kSets * kWarps * kSums * 4;
   static constexpr int kFit = (227 * 1024 - 1024 - kTableBytes - kPart - 256) / kSlot;
   static constexpr int kSlots = kFit > 7 ? 7 : kFit;
   static constexpr size_t kSmem = 1024 + kTableBytes + kPart + kSlots * kSlot;
@@ -104,11 +108,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
   constexpr int kN = kOne ? 1 : NB;
   constexpr bool kSplit = !kOne && FORMAT == kMxfp4 && XT == kF16;
   constexpr int TYPE = kSplit ? kBf16 : XT;
-  constexpr int kX = kN * 8;  // columns
   extern __shared__ __align__(16) uint8_t table[];  // first, so that its address is a constant of the lookups
-  float* part = reinterpret_cast<float*>(table + kTableBytes);  // [2][warps][32 rows][columns]
+  float* part = reinterpret_cast<float*>(table + kTableBytes);  // [sets][warps][tokens][32 rows, padded]
   const uint32_t ring = (smem_addr(table) + kTableBytes + S::kPart + 1023) & ~1023u;
-  __shared__ uint64_t full[S::kSlots], empty[S::kSlots];
+  __shared__ uint64_t full[S::kSlots], empty[S::kSlots], sums_full[S::kSets], sums_empty[S::kSets];
   __shared__ volatile uint32_t failed;
 
   const int warp = uniform_warp(), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -118,6 +121,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kSet);
+    }
+    for (int i = 0; i < S::kSets; ++i) {
+      mbar_init(&sums_full[i], kWarps);
+      mbar_init(&sums_empty[i], 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -168,6 +175,26 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
         }
       }
     }
+  } else if (warp == kWarps + 1) {
+    // ---- the sums of the warps, in their order, while those go on with the next unit: a lane
+    // a row
+    const float gamma = p.gamma ? *p.gamma : 1.0f;
+    Ring<S::kSets> r;
+    for (int u = first; u < p.units; u += step, r.next()) {
+      if (!__all_sync(0xFFFFFFFFu, wait(&sums_full[r.slot], r.phase, kSitePipeAcc))) break;
+      const int row = u * kRows + lane;
+      const float bias = p.bias && row < p.N ? load_value<XT>(p.bias, row) : 0.0f;
+      float* sums = part + r.slot * kWarps * S::kSums + lane;
+      for (int token = 0; token < p.batch; ++token) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) sum += sums[k * S::kSums + token * S::kPitch];
+        if (p.splits > 1) sums[token * S::kPitch] = sum;  // of this CTA's part of the reduction
+        else if (row < p.N) store_value<XT>(p.y, static_cast<size_t>(token) * p.N + row, fmaf(sum, gamma, bias));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sums_empty[r.slot]);
+    }
   } else {
     // ---- products: the 32 rows, values 128 kw .. of a stage.  An MMA's row g is row
     // g / 2 + 4 (g % 2) of its eight: the eight lanes of a 16-byte read then have two rows
@@ -177,7 +204,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
     // MXFP4: 128 values are one scale tile, the lane's block byte t; NVFP4: two tiles, the
     // lane's two blocks a half word of tile t / 2
     const uint32_t from_s = kStageBytes + (FORMAT == kMxfp4 ? kw : 2 * kw + (t >> 1)) * 512 + rr * 16;
-    const float gamma = p.gamma ? *p.gamma : 1.0f;
     // what a lane holds of x in a step: its 32 values of a token, or half of them or none
     uint4 x[kN][4];
 #pragma unroll
@@ -216,9 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
       }
     };
     Ring<S::kSlots> r;
-    int parity = 0, turn = 0;
+    Ring<S::kSets> sums;
+    int turn = 0;
     bool ok = true;
-    for (int u = first; u < p.units && ok; u += step, parity ^= 1) {
+    for (int u = first; u < p.units && ok; u += step, sums.next()) {
       float acc[2][kN][4] = {};
       for (int s = s0; s < s1; ++s, r.next(), turn ^= 1) {
         if (turn != set) continue;
@@ -298,40 +325,27 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[r.slot]);
       }
-      // ---- the unit's sums; the other half of `part` is still being read by slower warps
-      if constexpr (kOne) {  // the columns of a row are in its four lanes: all into column 0
+      if (!ok || !(ok = __all_sync(0xFFFFFFFFu, wait(&sums_empty[sums.slot], sums.phase ^ 1, kSitePipeAcc)))) break;
+      float* mine = part + (sums.slot * kWarps + warp) * S::kSums;
+      if constexpr (kOne) {  // the columns of a row are in its four lanes
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           float v = acc[h >> 1][0][2 * (h & 1)] + acc[h >> 1][0][2 * (h & 1) + 1];
           v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
           v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
-          if (t == 0) part[((parity * kWarps + warp) * kRows + h * 8 + rr) * kX] = v;
+          if (t == 0) mine[h * 8 + rr] = v;
         }
       } else {
-        float* mine = part + (parity * kWarps + warp) * kRows * kX;
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int n = 0; n < kN; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e)  // row 16 m + 8 (e / 2) + rr, token 8 n + 2 t + e % 2
-              mine[(m * 16 + (e >> 1) * 8 + rr) * kX + n * 8 + 2 * t + (e & 1)] = acc[m][n][e];
+              mine[(n * 8 + 2 * t + (e & 1)) * S::kPitch + m * 16 + (e >> 1) * 8 + rr] = acc[m][n][e];
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
-      float* sums = part + parity * kWarps * kRows * kX;
-      for (int e = threadIdx.x; e < kRows * p.batch; e += kConsumers) {
-        const int row = e % kRows, token = e / kRows;
-        float* at = sums + row * kX + token;
-        float sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) sum += at[k * kRows * kX];
-        if (p.splits > 1) {
-          at[0] = sum;
-        } else if (u * kRows + row < p.N) {
-          const float bias = p.bias ? load_value<XT>(p.bias, u * kRows + row) : 0.0f;
-          store_value<XT>(p.y, static_cast<size_t>(token) * p.N + u * kRows + row, fmaf(sum, gamma, bias));
-        }
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sums_full[sums.slot]);
     }
   }
   if (p.splits > 1) {  // of the one unit
@@ -341,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
     for (int e = rank * kThreads + threadIdx.x; e < kRows * p.batch; e += kThreads * p.splits) {
       const int row = e % kRows, token = e / kRows;
       if (first * kRows + row >= p.N) continue;
-      const uint32_t at = smem_addr(part + row * kX + token);
+      const uint32_t at = smem_addr(part + token * S::kPitch + row);
       float sum = 0.0f;
       for (int c = 0; c < p.splits; ++c) {
         float v;
