@@ -57,12 +57,13 @@ class Mx4Tensor:
         if p.dim() != 2 or p.shape[1] == 0 or p.shape[1] % 16 or p.shape[0] == 0:
             raise ValueError(f"packed must be [rows, K/2] with K a multiple of 32, got shape {tuple(p.shape)}")
         dev = p.device
-        _check_tensor(p, "packed", torch.uint8, dev)
-        _check_tensor(s, "scales", torch.uint8, dev, scale_tiles(p.shape[0], 2 * p.shape[1], self.format))
+        tiles = scale_tiles(p.shape[0], 2 * p.shape[1], self.format)
+        if not (p.dtype is s.dtype is torch.uint8 and s.shape == tiles and s.device == dev and p.is_contiguous()
+                and s.is_contiguous()):
+            _check_tensor(p, "packed", torch.uint8, dev)
+            _check_tensor(s, "scales", torch.uint8, dev, tiles)
         if g is not None:
-            _check_tensor(g, "tensor_scale", torch.float32, dev)
-            if g.numel() != 1:
-                raise ValueError(f"tensor_scale must hold one value, got shape {tuple(g.shape)}")
+            _check_scale(g, dev)
 
     @classmethod
     def _of(cls, packed, scales, format, tensor_scale) -> "Mx4Tensor":
@@ -114,29 +115,27 @@ def _check(status: int, what: str):
         raise native.AqlmError(status, what)
 
 
-class _Here:
-    """No change of device or stream."""
-
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
+def _check_scale(g: torch.Tensor, dev):
+    _check_tensor(g, "tensor_scale", torch.float32, dev)
+    if g.numel() != 1:
+        raise ValueError(f"tensor_scale must hold one value, got shape {tuple(g.shape)}")
 
 
-_HERE = _Here()
+def _elsewhere(dev: torch.device, stream: Optional[torch.cuda.Stream]) -> bool:
+    """Whether a call has to change the current device or stream: the library launches on the
+    current device, and what a call allocates belongs to the stream that it runs on."""
+    return stream is not None or dev.type != "cuda" or dev.index != torch.cuda.current_device()
 
 
 def _on(dev: torch.device, stream: Optional[torch.cuda.Stream]):
-    """The context that a call runs in: the library launches on the current device, and what
-    a call allocates belongs to the stream that it runs on."""
+    """The context that makes them current."""
     if dev.type != "cuda":
         raise ValueError(f"mx4 tensors must live on a CUDA device, got {dev}")
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        return torch.cuda.stream(stream)  # sets the device too
-    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)  # sets the device too
 
 
 # The handle of a device's current stream (torch.cuda.current_stream builds an object, which
@@ -170,18 +169,19 @@ def quantize(x: torch.Tensor, format: Format, tensor_scale: Optional[torch.Tenso
     if tensor_scale is not None:
         if fmt == Format.MXFP4:
             raise ValueError("MXFP4 is quantised without a tensor scale")
-        _check_tensor(tensor_scale, "tensor_scale", torch.float32, dev)
-        if tensor_scale.numel() != 1:
-            raise ValueError(f"tensor_scale must hold one value, got shape {tuple(tensor_scale.shape)}")
-    with _on(dev, stream):
-        if out is None:
-            out = Mx4Tensor._of(torch.empty((rows, K // 2), dtype=torch.uint8, device=dev),
-                                torch.empty(scale_tiles(rows, K, fmt), dtype=torch.uint8, device=dev), fmt, tensor_scale)
-        elif (out.rows, out.K, out.format, out.device) != (rows, K, fmt, dev) or \
-                _ptr(out.tensor_scale) != _ptr(tensor_scale):
-            raise ValueError("out must have x's rows and K, its device, the format and the tensor scale of the call")
-        _check(native.lib().mx4_quantize(x.data_ptr(), xt, out.packed.data_ptr(), out.scales.data_ptr(),
-                                         _ptr(tensor_scale), rows, K, fmt, _current(dev.index)), "mx4_quantize")
+        _check_scale(tensor_scale, dev)
+    if out is not None and ((out.rows, out.K, out.format, out.device) != (rows, K, fmt, dev) or
+                            _ptr(out.tensor_scale) != _ptr(tensor_scale)):
+        raise ValueError("out must have x's rows and K, its device, the format and the tensor scale of the call")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return quantize(x, fmt, tensor_scale, out)
+    if out is None:
+        up, across, _ = scale_tiles(rows, K, fmt)
+        out = Mx4Tensor._of(torch.empty(rows, K // 2, dtype=torch.uint8, device=dev),
+                            torch.empty(up, across, 512, dtype=torch.uint8, device=dev), fmt, tensor_scale)
+    _check(native.lib().mx4_quantize(x.data_ptr(), xt, out.packed.data_ptr(), out.scales.data_ptr(),
+                                     _ptr(tensor_scale), rows, K, fmt, _current(dev.index)), "mx4_quantize")
     return out
 
 
@@ -192,14 +192,15 @@ def dequantize(t: Mx4Tensor, dtype: torch.dtype = torch.float16, out: Optional[t
     packed = t.packed
     dev = packed.device
     rows, half = packed.shape
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((rows, 2 * half), dtype=dtype, device=dev)
-        else:
-            _check_tensor(out, "out", dtype, dev, (rows, 2 * half))
-        _check(native.lib().mx4_dequantize(packed.data_ptr(), t.scales.data_ptr(), _ptr(t.tensor_scale),
-                                           out.data_ptr(), code, rows, 2 * half, t.format, _current(dev.index)),
-               "mx4_dequantize")
+    if out is not None:
+        _check_tensor(out, "out", dtype, dev, (rows, 2 * half))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return dequantize(t, dtype, out)
+    if out is None:
+        out = torch.empty(rows, 2 * half, dtype=dtype, device=dev)
+    _check(native.lib().mx4_dequantize(packed.data_ptr(), t.scales.data_ptr(), _ptr(t.tensor_scale), out.data_ptr(),
+                                       code, rows, 2 * half, t.format, _current(dev.index)), "mx4_dequantize")
     return out
 
 
@@ -239,24 +240,26 @@ def matmul(x: Union[torch.Tensor, Mx4Tensor], w: Mx4Tensor, bias: Optional[torch
         out_dtype = x.dtype
     if bias is not None:
         _check_tensor(bias, "bias", out_dtype, dev, (N,))
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((batch, N), dtype=out_dtype, device=dev)
-        else:
-            _check_tensor(out, "out", out_dtype, dev, (batch, N))
-        if four:
-            _check(native.lib().mx4_matmul_mx4(x.packed.data_ptr(), x.scales.data_ptr(), _ptr(x.tensor_scale),
-                                               packed.data_ptr(), w.scales.data_ptr(), _ptr(w.tensor_scale),
-                                               _ptr(bias), out.data_ptr(), code, N, K, batch, w.format,
-                                               _current(dev.index)), "mx4_matmul_mx4")
-        else:
-            ws, need = None, 0
-            if code == 0 and not w.format:  # fp16 x with MXFP4 weights alone can need one
-                need = native.mx4_matmul_workspace_size(code, N, K, batch, w.format)
-                ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-            _check(native.lib().mx4_matmul(x.data_ptr(), code, packed.data_ptr(), w.scales.data_ptr(),
-                                           _ptr(w.tensor_scale), _ptr(bias), out.data_ptr(), N, K, batch, w.format,
-                                           _ptr(ws), need, _current(dev.index)), "mx4_matmul")
+    if out is not None:
+        _check_tensor(out, "out", out_dtype, dev, (batch, N))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return matmul(x, w, bias, out, out_dtype)
+    if out is None:
+        out = torch.empty(batch, N, dtype=out_dtype, device=dev)
+    if four:
+        _check(native.lib().mx4_matmul_mx4(x.packed.data_ptr(), x.scales.data_ptr(), _ptr(x.tensor_scale),
+                                           packed.data_ptr(), w.scales.data_ptr(), _ptr(w.tensor_scale), _ptr(bias),
+                                           out.data_ptr(), code, N, K, batch, w.format, _current(dev.index)),
+               "mx4_matmul_mx4")
+    else:
+        ws, need = None, 0
+        if code == 0 and not w.format:  # fp16 x with MXFP4 weights alone can need one
+            need = native.mx4_matmul_workspace_size(code, N, K, batch, w.format)
+            ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+        _check(native.lib().mx4_matmul(x.data_ptr(), code, packed.data_ptr(), w.scales.data_ptr(),
+                                       _ptr(w.tensor_scale), _ptr(bias), out.data_ptr(), N, K, batch, w.format,
+                                       _ptr(ws), need, _current(dev.index)), "mx4_matmul")
     return out
 
 
@@ -272,14 +275,16 @@ def input_grad(dy: torch.Tensor, w: Mx4Tensor, out: Optional[torch.Tensor] = Non
     batch = dy.shape[0]
     if batch == 0:
         raise ValueError("dy must have at least one row")
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((batch, 2 * half), dtype=dy.dtype, device=dev)
-        else:
-            _check_tensor(out, "out", dy.dtype, dev, (batch, 2 * half))
-        need = native.mx4_input_grad_workspace_size(code, N, 2 * half, batch, w.format)
-        ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-        _check(native.lib().mx4_input_grad(dy.data_ptr(), code, packed.data_ptr(), w.scales.data_ptr(),
-                                           _ptr(w.tensor_scale), out.data_ptr(), N, 2 * half, batch, w.format,
-                                           _ptr(ws), need, _current(dev.index)), "mx4_input_grad")
+    if out is not None:
+        _check_tensor(out, "out", dy.dtype, dev, (batch, 2 * half))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return input_grad(dy, w, out)
+    if out is None:
+        out = torch.empty(batch, 2 * half, dtype=dy.dtype, device=dev)
+    need = native.mx4_input_grad_workspace_size(code, N, 2 * half, batch, w.format)
+    ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    _check(native.lib().mx4_input_grad(dy.data_ptr(), code, packed.data_ptr(), w.scales.data_ptr(),
+                                       _ptr(w.tensor_scale), out.data_ptr(), N, 2 * half, batch, w.format, _ptr(ws),
+                                       need, _current(dev.index)), "mx4_input_grad")
     return out
