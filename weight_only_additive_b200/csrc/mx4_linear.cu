@@ -565,35 +565,36 @@ struct Tiling {
   bool table;
 };
 
-// Tokens of a tile, pairs and the split of the reduction.  A pair's stages hold 256 tokens, a
-// CTA's 128 (192 for dx, whose stages are half as deep), or 64 beside the table; half of that
-// for two parts.
+// Tokens of a tile, pairs, lookup decoding and the split of the reduction: the least time of
+// rounds over the SMs, in cycles, by what 128 values of the reduction take and what the launch
+// and a tile take besides.  Measured with 4096 to 14336 features: 5.3 cycles a token of the tile,
+// but at least 840 with the table and 1400 without (dx: 1200 and 1550), which is the
+// decoding, and 250 more for x in two parts.
+// So pairs with the table take the middle (512 tokens, 4096 x 4096: 21 us, 28 without, 33 by
+// single CTAs), wide tiles without it the large batches (2048 x 4096 x 11008: 126 us, 149 with).
 Tiling plan(int features, int depth, int batch, int parts, bool grad) {
   const int slots = (depth + kSlotDepth - 1) / kSlotDepth;
-  const int f_tiles = (features + kF - 1) / kF;
-  const auto even = [&](int most, int unit) {
-    const int t_tiles = (batch + most - 1) / most;
-    return ((batch + t_tiles - 1) / t_tiles + unit - 1) / unit * unit;
-  };
-  if (batch > 128) {
-    // rounds of pairs over the SMs times a stage's time: its MMAs, or the decoding where the
-    // tile is narrower than that takes, and a little for every stage
-    int nt = 0;
-    long long best = 0;
-    for (int n = 256 / parts; n >= 64; n -= 16) {
-      const long long tiles = static_cast<long long>(f_tiles + 1) / 2 * ((batch + n - 1) / n);
-      const long long cost = (tiles + kSms / 2 - 1) / (kSms / 2) * ((n * parts > 208 ? n * parts : 208) + 16);
-      if (!best || cost < best) best = cost, nt = n;
+  Tiling best{};
+  double least = 0;
+  for (int cg = 1; cg <= 2; ++cg) {
+    const long long f_tiles = (features + kF * cg - 1) / (kF * cg);
+    for (int table = 0; table <= 1; ++table) {
+      const int most = (table ? 64 : grad && cg == 1 ? 192 : 128) * cg / parts;
+      const double decode = (table ? grad ? 1200 : 840 : grad ? 1550 : 1400) + (parts > 1 ? 250 : 0);
+      for (int t_tiles = (batch + most - 1) / most, more = 0; more < 6; ++more, ++t_tiles) {
+        const int nt = ((batch + t_tiles - 1) / t_tiles + 15) / 16 * 16;
+        const long long tiles = f_tiles * ((batch + nt - 1) / nt);
+        const double mma = 5.3 * nt * parts, stage = mma > decode ? mma : decode;
+        for (int splits = 1; splits <= (cg == 1 ? 8 : 1); splits *= 2) {
+          if (splits > 1 && (tiles * splits > kSms || slots < 2 * splits)) break;
+          const long long rounds = (tiles * cg * splits + kSms - 1) / kSms;
+          const double cost = rounds * (2.0 * ((slots + splits - 1) / splits) * stage + 1500) + 9000 + (splits > 1 ? 1500 : 0);
+          if (least == 0 || cost < least) least = cost, best = Tiling{nt, cg, splits, table != 0};
+        }
+      }
     }
-    if (static_cast<long long>(f_tiles + 1) / 2 * ((batch + nt - 1) / nt) >= kSms / 4) return {nt, 2, 1, false};
   }
-  const bool table = batch <= 64 / parts;
-  const int nt = even(table ? 64 / parts : (grad ? 192 : 128) / parts, 16);
-  const int t_tiles = (batch + nt - 1) / nt;
-  int splits = 1;
-  while (splits < 8 && static_cast<long long>(f_tiles) * t_tiles * splits * 2 <= kSms && slots >= 2 * splits * 2)
-    splits *= 2;
-  return {nt, 1, splits, table};
+  return best;
 }
 
 cudaError_t map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* p, uint64_t cols, uint64_t rows, uint64_t pitch,
@@ -663,9 +664,11 @@ template <bool GRAD>
 cudaError_t run(const Call& c, uint32_t* status, cudaStream_t stream) {
   const Tiling tl = plan(c.features, c.depth, c.batch, split_parts(c.type, c.format) ? 2 : 1, GRAD);
 #define MX4_CASE(f, t)                                                                     \
-  return tl.cg == 2   ? launch_linear<f, t, GRAD, 2, false>(c, tl, status, stream)         \
-         : tl.table   ? launch_linear<f, t, GRAD, 1, true>(c, tl, status, stream)          \
-                      : launch_linear<f, t, GRAD, 1, false>(c, tl, status, stream);
+  if (tl.table)                                                                            \
+    return tl.cg == 2 ? launch_linear<f, t, GRAD, 2, true>(c, tl, status, stream)          \
+                      : launch_linear<f, t, GRAD, 1, true>(c, tl, status, stream);         \
+  return tl.cg == 2 ? launch_linear<f, t, GRAD, 2, false>(c, tl, status, stream)           \
+                    : launch_linear<f, t, GRAD, 1, false>(c, tl, status, stream);
   if (c.format == kMxfp4) { MX4_CASE(kMxfp4, kBf16) }
   if (c.type == kF16) { MX4_CASE(kNvfp4, kF16) }
   MX4_CASE(kNvfp4, kBf16)
