@@ -459,12 +459,13 @@ def mlp(x, up, down, b):
 
 
 @pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("dtype", TYPES[:2])
 @pytest.mark.parametrize("batch", [1, 13, 150])
-def test_run_together_on_streams_and_in_graphs(dev, fmt, batch):
+def test_run_together_on_streams_and_in_graphs(dev, fmt, dtype, batch):
     up, _ = ordinary(512, 256, fmt, 20, dev)
     down, _ = ordinary(256, 512, fmt, 21, dev)
-    b = torch.randn((512,), generator=gen(22)).to(dev, torch.bfloat16)
-    xs = [torch.randn((batch, 256), generator=gen(23, i)).to(dev, torch.bfloat16) for i in range(3)]
+    b = torch.randn((512,), generator=gen(22)).to(dev, dtype)
+    xs = [torch.randn((batch, 256), generator=gen(23, i)).to(dev, dtype) for i in range(3)]
     want = [mlp(x, up, down, b) for x in xs]
     torch.cuda.synchronize()
     # two streams at once, many times over
@@ -496,7 +497,7 @@ def test_run_together_on_streams_and_in_graphs(dev, fmt, batch):
     for k in range(2):
         assert all(torch.equal(p, q) for p, q in zip(graphs[k][2], want[2 - k]))
     # an explicit stream, and buffers of the caller's
-    y = torch.empty((batch, 512), dtype=torch.bfloat16, device=dev)
+    y = torch.empty((batch, 512), dtype=dtype, device=dev)
     s1.wait_stream(torch.cuda.current_stream())
     assert mx4.matmul(xs[0], up, b, out=y, stream=s1) is y
     s1.synchronize()

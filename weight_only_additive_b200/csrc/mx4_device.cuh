@@ -151,6 +151,17 @@ __device__ __forceinline__ bool mbar_wait_sleeping(uint64_t* bar, uint32_t parit
   return true;
 }
 
+// The end of all roles of a CTA.  After a wait that gave up, the copies and MMAs still in flight
+// get a millisecond to end before the shared and tensor memory go away.
+__device__ __forceinline__ void settle_after_failure(volatile uint32_t& failed) {
+  __syncthreads();
+  if (failed) {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000) {
+    }
+  }
+}
+
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;

@@ -155,9 +155,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
       const uint64_t pol = l2_policy_evict_first();
       Ring<S::kSlots> r;
       bool ok = true;
-      uint32_t issued = 0;
       for (int u = first; u < p.units && ok; u += step)
-        for (int s = s0; s < s1; ++s, r.next(), ++issued) {
+        for (int s = s0; s < s1; ++s, r.next()) {
           ok = wait(&empty[r.slot], r.phase ^ 1, kSitePipeEmpty);
           if (!ok) break;
           const uint32_t at = ring + r.slot * S::kSlot;
@@ -169,11 +168,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
           bulk_load(at + kStageBytes, p.scales + (static_cast<size_t>(u >> 2) * p.tiles + s * S::kTiles) * 512, run,
                     &full[r.slot]);
         }
-      if (!ok && issued) {  // what was asked for lands before the shared memory goes away
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 1000000) {
-        }
-      }
     }
   } else if (warp == kWarps + 1) {
     // ---- the sums of the warps, in their order, while those go on with the next unit: a lane
@@ -348,8 +342,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
       if (lane == 0) mbar_arrive(&sums_full[sums.slot]);
     }
   }
+  __syncwarp();
+  settle_after_failure(failed);
   if (p.splits > 1) {  // of the one unit
-    __syncwarp();
     cluster_sync();
     const float gamma = p.gamma ? *p.gamma : 1.0f;
     for (int e = rank * kThreads + threadIdx.x; e < kRows * p.batch; e += kThreads * p.splits) {

@@ -256,12 +256,11 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
     // ---- activations
     const uint64_t keep = l2_policy_evict_last();
     Ring<kRing> r;
-    uint32_t issued = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
       const int row = tokens_at(t) + (CG > 1 ? rank * (p.nt / CG) : 0);
       for (int s = s0; s < s1 && ok; ++s)
-        for (int j = 0; j < S::kSlotStages; ++j, r.next(), ++issued) {
+        for (int j = 0; j < S::kSlotStages; ++j, r.next()) {
           ok = wait(&done[r.slot], r.phase ^ 1, kSitePipeEmpty);
           if (!ok) break;
           uint32_t at = smem + S::kX + r.slot * x_stage;
@@ -272,22 +271,15 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
               tma_load_2d(at, &x_map, s * kSlotDepth + j * S::kDepth + h * 64, row + q * p.batch, &ready[r.slot], keep);
         }
     }
-    // after a failure what was asked for lands before the shared memory goes away
-    if (!ok && issued) {
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 1000000) {
-      }
-    }
   } else if (warp == kWarpW && lane == 0) {
     // ---- packed weights and scales
     const uint64_t pol = p.t_tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
     const int row_tiles = ((GRAD ? p.depth : p.features) + 127) / 128;
     Ring<S::kWSlots> r;
-    uint32_t issued = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
       const int f0 = features_at(t);
-      for (int s = s0; s < s1; ++s, r.next(), ++issued) {
+      for (int s = s0; s < s1; ++s, r.next()) {
         ok = wait(&w_empty[r.slot], r.phase ^ 1, kSitePipeCodes);
         if (!ok) break;
         const uint32_t at = smem + S::kW + r.slot * kSlotBytes, sc = smem + S::kS + r.slot * kSlotScales;
@@ -304,11 +296,6 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
         else tma_load_2d(at, &w_map, s * (kSlotDepth / 2), f0, full, pol);
         for (int q = 0; q < rows; ++q)
           bulk_load(sc + q * (kSlotScales / 2), p.scales + (static_cast<size_t>(r0 + q) * p.tiles + c0) * 512, run, full);
-      }
-    }
-    if (!ok && issued) {
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 1000000) {
       }
     }
   } else if (warp == kWarpMma && CG > 1 && rank > 0) {
@@ -491,6 +478,7 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
   }
 
   __syncwarp();
+  settle_after_failure(failed);
   if (CG == 1 && p.splits > 1) {
     cluster_sync();
     const int f0 = features_at(first), t0 = tokens_at(first);
@@ -582,7 +570,7 @@ Tiling plan(int features, int depth, int batch, int parts, bool grad) {
       const int most = (table ? 64 : grad && cg == 1 ? 192 : 128) * cg / parts;
       const double decode = (table ? grad ? 1200 : 840 : grad ? 1550 : 1400) + (parts > 1 ? 250 : 0);
       for (int t_tiles = (batch + most - 1) / most, more = 0; more < 6; ++more, ++t_tiles) {
-        const int nt = ((batch + t_tiles - 1) / t_tiles + 15) / 16 * 16;
+        const int unit = 16 * cg, nt = ((batch + t_tiles - 1) / t_tiles + unit - 1) / unit * unit;
         const long long tiles = f_tiles * ((batch + nt - 1) / nt);
         const double mma = 5.3 * nt * parts, stage = mma > decode ? mma : decode;
         for (int splits = 1; splits <= (cg == 1 ? 8 : 1); splits *= 2) {

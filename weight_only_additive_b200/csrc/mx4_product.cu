@@ -207,11 +207,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const uint64_t keep = l2_policy_evict_last(), pass = l2_policy_evict_first();
     const int w_row_tiles = (p.N + 127) / 128, x_row_tiles = (p.batch + 127) / 128;
     Ring<P::kStages> r;
-    uint32_t issued = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
       const int m = (t % p.m_tiles) * CG + pair_rank, n0 = (t / p.m_tiles) * NT;
-      for (int s = s0; s < s1; ++s, r.next(), ++issued) {
+      for (int s = s0; s < s1; ++s, r.next()) {
         ok = wait(&empty[r.slot], r.phase ^ 1, kSitePipeEmpty);
         if (!ok) break;
         uint64_t* bar = &full[r.slot];
@@ -228,12 +227,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         if (x_tiles) bulk_load(sa, p.xs + (static_cast<size_t>(m) * p.tiles + c0) * 512, run, bar);
         for (int j = 0; j < w_tiles; ++j)
           bulk_load(sb + j * P::kSa, p.ws + (static_cast<size_t>(wt + j) * p.tiles + c0) * 512, run, bar);
-      }
-    }
-    // after a failure what was asked for lands before the shared memory goes away
-    if (!ok && issued) {
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 1000000) {
       }
     }
   } else if (warp == 1 && CG > 1 && rank > 0) {
@@ -344,6 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
   }
 
+  __syncwarp();
+  settle_after_failure(failed);
   if (p.splits > 1) {
     // the partial tiles of the cluster, added in rank order
     __syncwarp();
