@@ -9,6 +9,10 @@
 // tiles, which tcgen05.cp spreads over the four TMEM lane quadrants as the MMA wants
 // them.  One thread loads, one issues copies and MMAs, eight warps write results.
 //
+// Rows of y that are not whole 16-byte units would be written value by value, a row a lane.
+// There the operands change places: a lane then has a feature, and a warp writes 32 neighbours
+// of one token (388 x 9839 x 1472: 13 us, 75 by rows).
+//
 // Work: one CTA per output tile, persistent over the SMs; where there are fewer tiles
 // than SMs a cluster of CTAs shares a tile along K and adds the fp32 partial tiles through
 // distributed shared memory, in rank order, so results do not depend on timing.
@@ -58,8 +62,9 @@ struct ProductParams {
   const void* bias;
   void* y;
   uint32_t* status;
-  int batch, N, K, tiles;  // tiles: scale tiles along K
+  int batch, N, K, tiles;  // rows of the first and second operand; scale tiles along K
   int m_tiles, n_tiles, splits, y_type;
+  bool swapped;            // the first operand is the weights: y is [N][batch]
 };
 
 // Shared-memory descriptor of a 512-byte scale tile: 32 rows of 16 bytes, 8-row groups 128
@@ -112,6 +117,21 @@ __device__ __forceinline__ void bias8(const void* bias, int type, size_t c, floa
       b[2 * i] = f.x, b[2 * i + 1] = f.y;
     }
   }
+}
+
+// One value of a swapped product: y[c][row].
+__device__ __forceinline__ void put_swapped(const ProductParams& p, int row, int c, float v, float scale, float bias) {
+  const size_t at = static_cast<size_t>(c) * p.batch + row;
+  const float r = fmaf(v, scale, bias);
+  if (p.y_type == kF32) store_value<kF32>(p.y, at, r);
+  else if (p.y_type == kF16) store_value<kF16>(p.y, at, r);
+  else store_value<kBf16>(p.y, at, r);
+}
+__device__ __forceinline__ float bias_of(const ProductParams& p, int i) {
+  return !p.bias ? 0.0f
+         : p.y_type == kF32 ? load_value<kF32>(p.bias, i)
+         : p.y_type == kF16 ? load_value<kF16>(p.bias, i)
+                            : load_value<kBf16>(p.bias, i);
 }
 
 // v[0..8) * scale + bias to y[row][c ..); `vec`: rows of y are whole 16-byte units.
@@ -328,6 +348,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(stages) + (quad * 32 + lane) * P::kRedPitch + c);
 #pragma unroll
           for (int e = 0; e < 8; ++e) q[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+        } else if (p.swapped) {
+          if (row < p.batch) {
+            const float bias = bias_of(p, row);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (n0 + c + e < p.N) put_swapped(p, row, n0 + c + e, f[e], scale, bias);
+          }
         } else if (row < p.batch) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -340,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   __syncwarp();
   settle_after_failure(failed);
   if (p.splits > 1) {
-    // the partial tiles of the cluster, added in rank order
+    // the partial tiles of the cluster, added in rank order: eight columns of a row a thread
     __syncwarp();
     cluster_sync();
     const int m0 = (first % p.m_tiles) * kRows, n0 = (first / p.m_tiles) * NT;
@@ -350,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     if (p.gx) scale *= *p.gx;
     const uint32_t red = smem_addr(stages);
     for (int e = rank * kThreads + threadIdx.x; e < rows * (NT / 8); e += kThreads * p.splits) {
-      const int r = e / (NT / 8), c = e % (NT / 8) * 8;
+      const int r = p.swapped ? e % rows : e / (NT / 8), c = (p.swapped ? e / rows : e % (NT / 8)) * 8;
       if (c >= cols) continue;
       float v[8] = {};
       for (int s = 0; s < p.splits; ++s) {
@@ -359,7 +386,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
         v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
       }
-      put8(p, m0 + r, n0 + c, v, scale, vec);
+      if (p.swapped) {
+        const float bias = bias_of(p, m0 + r);
+        for (int i = 0; i < 8; ++i)
+          if (c + i < cols) put_swapped(p, m0 + r, n0 + c + i, v[i], scale, bias);
+      } else {
+        put8(p, m0 + r, n0 + c, v, scale, vec);
+      }
     }
     cluster_sync();  // no CTA leaves while another reads its partial tile
   }
@@ -387,29 +420,32 @@ cudaError_t packed_map(CUtensorMap* map, const Mx4& t, int K, int box) {
 
 constexpr int kSms = 148;
 
+// a: the operand of 128-row tiles, b: that of NT; the activations and the weights, or swapped.
 template <int FORMAT, int NT, int CG = 1>
-cudaError_t product_as(const Mx4Product& p, int splits, uint32_t* status, cudaStream_t stream) {
+cudaError_t product_as(const Mx4Product& p, const Mx4& a, const Mx4& b, bool swapped, int splits, uint32_t* status,
+                       cudaStream_t stream) {
   using P = Plan<FORMAT, NT, CG>;
-  CUtensorMap x_map, w_map;
-  cudaError_t e = packed_map(&x_map, p.x, p.K, kRows);
-  if (e == cudaSuccess) e = packed_map(&w_map, p.w, p.K, NT / CG);
+  CUtensorMap a_map, b_map;
+  cudaError_t e = packed_map(&a_map, a, p.K, kRows);
+  if (e == cudaSuccess) e = packed_map(&b_map, b, p.K, NT / CG);
   if (e != cudaSuccess) return e;
   ProductParams q{};
-  q.xs = p.x.scales;
-  q.ws = p.w.scales;
+  q.xs = a.scales;
+  q.ws = b.scales;
   q.gx = p.x.tensor_scale;
   q.gw = p.w.tensor_scale;
   q.bias = p.bias;
   q.y = p.y;
   q.status = status;
-  q.batch = p.x.rows;
-  q.N = p.w.rows;
+  q.batch = a.rows;
+  q.N = b.rows;
   q.K = p.K;
   q.tiles = mx4_scale_tiles(p.K, FORMAT);
   q.m_tiles = (q.batch + kRows * CG - 1) / (kRows * CG);
   q.n_tiles = (q.N + NT - 1) / NT;
   q.splits = splits;
   q.y_type = p.y_type;
+  q.swapped = swapped;
   auto* kernel = product_kernel<FORMAT, NT, CG>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(P::kSmem));
   if (e != cudaSuccess) return e;
@@ -417,19 +453,25 @@ cudaError_t product_as(const Mx4Product& p, int splits, uint32_t* status, cudaSt
   if (tiles > 0x7FFFFFFF / 8) return cudaErrorInvalidValue;
   const long long ctas = tiles * CG * splits;
   const unsigned grid = static_cast<unsigned>(splits > 1 || ctas < kSms ? ctas : kSms);
-  return launch_overlapped(kernel, grid, kThreads, P::kSmem, stream, CG * splits, x_map, w_map, q);
+  return launch_overlapped(kernel, grid, kThreads, P::kSmem, stream, CG * splits, a_map, b_map, q);
 }
 
-// Tile width and K split.  A tile's time is its MMAs (2 cycles per feature and 64 values
-// of K at a rate of 128 x 256 x 64 in 128 cycles) or its loads, plus filling and draining.
+// Tile width and K split.  A tile's time is its MMAs (2 cycles per column and 64 values of K at
+// a rate of 128 x 256 x 64 in 128 cycles) or its loads, plus filling and draining.  Forcing each
+// width and split on 1 to 1000 tokens of 4096 to 14336 features found nothing more than 15 %
+// faster than what this picks (64 x 14336 x 4096: 128 wide 9.4 us, 64 wide 13.5, 256 wide 12.5;
+// 64 x 4096 x 14336: 128 wide, K in four, 11.5, unsplit 20.7; 4096 x 28672 x 8192: pairs 400,
+// single 508).
 template <int FORMAT>
 cudaError_t product_planned(const Mx4Product& p, uint32_t* status, cudaStream_t stream) {
-  const long long m_tiles = (p.x.rows + kRows - 1) / kRows;
+  const bool swapped = p.w.rows % (p.y_type == kF32 ? 4 : 8) != 0;
+  const Mx4 &a = swapped ? p.w : p.x, &b = swapped ? p.x : p.w;
+  const long long m_tiles = (a.rows + kRows - 1) / kRows;
   const int k_stages = (p.K + kStageK - 1) / kStageK;
   int best_nt = 256, best_split = 1;
   double best = 1e300;
   for (int nt : {64, 128, 192, 256}) {
-    const long long tiles = m_tiles * ((p.w.rows + nt - 1) / nt);
+    const long long tiles = m_tiles * ((b.rows + nt - 1) / nt);
     for (int split : {1, 2, 4, 8}) {
       if (split > 1 && (tiles * split > kSms || k_stages < 2 * split || nt > 128)) continue;
       const double waves = static_cast<double>((tiles * split + kSms - 1) / kSms);
@@ -440,13 +482,13 @@ cudaError_t product_planned(const Mx4Product& p, uint32_t* status, cudaStream_t 
       if (cost < best) best = cost, best_nt = nt, best_split = split;
     }
   }
-  const long long pairs = (m_tiles + 1) / 2 * ((p.w.rows + 255) / 256);
-  if (m_tiles > 1 && pairs >= kSms / 4) return product_as<FORMAT, 256, 2>(p, 1, status, stream);
+  const long long pairs = (m_tiles + 1) / 2 * ((b.rows + 255) / 256);
+  if (m_tiles > 1 && pairs >= kSms / 4) return product_as<FORMAT, 256, 2>(p, a, b, swapped, 1, status, stream);
   switch (best_nt) {
-    case 64: return product_as<FORMAT, 64>(p, best_split, status, stream);
-    case 128: return product_as<FORMAT, 128>(p, best_split, status, stream);
-    case 192: return product_as<FORMAT, 192>(p, best_split, status, stream);
-    default: return product_as<FORMAT, 256>(p, best_split, status, stream);
+    case 64: return product_as<FORMAT, 64>(p, a, b, swapped, best_split, status, stream);
+    case 128: return product_as<FORMAT, 128>(p, a, b, swapped, best_split, status, stream);
+    case 192: return product_as<FORMAT, 192>(p, a, b, swapped, best_split, status, stream);
+    default: return product_as<FORMAT, 256>(p, a, b, swapped, best_split, status, stream);
   }
 }
 
