@@ -243,6 +243,11 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[N][32]) {
     for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(v[i][j]));
 }
 
+// Fetches a tensor map ahead of the first copy that uses it.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // Launch with programmatic stream serialisation: the kernel's start overlaps the end of
 // the one before it, and its grid_dependency_wait() orders its memory accesses after it.
 template <typename... Params, typename... Args>

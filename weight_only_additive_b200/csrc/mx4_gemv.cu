@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == kWarps && lane == 0) prefetch_map(&w_map);
   const uint32_t lane4 = lane * 4;
   if (warp < kWarps) {  // the table: each warp's 16 bytes, decoded by a lane each
     uint32_t h[4];
@@ -134,12 +135,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
       *reinterpret_cast<uint32_t*>(table + (warp * 16 + b) * 256 + lane4) = __shfl_sync(0xFFFFFFFFu, h[0], b);
   }
   __syncthreads();
-  grid_dependency_wait();
-  grid_dependents_launch();
 
   const int stages = (p.K + kStage - 1) / kStage, chunks = p.K / 32;
   const int s0 = stages * rank / p.splits, s1 = stages * (rank + 1) / p.splits;
   const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
+
+  grid_dependency_wait();
+  grid_dependents_launch();
+
   const auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
     if (mbar_wait_sleeping<false>(bar, parity, p.status, site, &failed)) return true;
     failed = 1;

@@ -208,6 +208,8 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kWarpMma) tmem_alloc_cg<CG>(&tmem_slot, 512);
+  if (warp == kWarpX && lane == 0) prefetch_map(&x_map);
+  if (warp == kWarpW && lane == 0) prefetch_map(&w_map);
   const uint32_t lane4 = lane * 4;
   if (TABLE && warp >= kWarpDecode && warp < kWarpOut) {  // a warp's 16 bytes, decoded by a lane each
     const int b0 = (warp - kWarpDecode) * 16;
@@ -223,9 +225,6 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
   tc_fence_after_sync();
   const uint32_t tmem = tmem_slot;
 
-  grid_dependency_wait();
-  grid_dependents_launch();
-
   const int slots = (p.depth + kSlotDepth - 1) / kSlotDepth;
   const int k_rank = CG > 1 ? 0 : rank;
   const int s0 = slots * k_rank / p.splits, s1 = slots * (k_rank + 1) / p.splits;
@@ -236,6 +235,9 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
   const uint32_t acc_cols = GRAD ? 256 : 128;
   const uint32_t x_box = static_cast<uint32_t>(p.nt / CG) * 128;          // bytes of 64 values of the tile's tokens
   const uint32_t x_part = x_box * (S::kDepth / 64), x_stage = x_part * p.parts;
+  grid_dependency_wait();
+  grid_dependents_launch();
+
   const auto features_at = [&](int t) { return (t / p.t_tiles) * kF * CG + (CG > 1 ? rank * kF : 0); };
   const auto tokens_at = [&](int t) { return (t % p.t_tiles) * p.nt; };
   // a wait that gives up makes every later one of this CTA that is not over end soon
@@ -441,13 +443,13 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
     uint32_t n_acc = 0;
     for (int t = first; t < total; t += step, ++n_acc) {
       const uint32_t acc = accs == 2 ? n_acc & 1 : 0, acc_phase = accs == 2 ? (n_acc >> 1) & 1 : n_acc & 1;
-      if (!warp_ok([&] { return wait(&acc_full[acc], acc_phase, kSitePipeAcc); })) break;
-      tc_fence_after_sync();
       const int f = features_at(t) + quad * 32 + lane, t0 = tokens_at(t);
       const int tokens = min(p.nt, p.batch - t0);
       const bool real = f < p.features;
       float bias = 0.0f;
       if (p.bias && real) bias = p.out_type == kF16 ? load_value<kF16>(p.bias, f) : load_value<kBf16>(p.bias, f);
+      if (!warp_ok([&] { return wait(&acc_full[acc], acc_phase, kSitePipeAcc); })) break;
+      tc_fence_after_sync();
       const uint32_t d = tmem + acc * acc_cols + (static_cast<uint32_t>(quad * 32) << 16);
 #pragma unroll 1
       for (int c = 0; c < p.nt; c += 16) {

@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 0 && lane == 0) prefetch_map(&x_map), prefetch_map(&w_map);
   if (warp == 1) tmem_alloc_cg<CG>(&tmem_slot, P::kCols);
   tc_fence_before_sync();
   __syncthreads();
@@ -201,15 +202,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   const uint32_t tmem = tmem_slot;
   const uint32_t scale_tmem = tmem + P::kAccs * NT;
 
-  grid_dependency_wait();
-  grid_dependents_launch();
-
   const int k_stages = (p.K + kStageK - 1) / kStageK;
   const int k_rank = CG > 1 ? 0 : rank, pair_rank = CG > 1 ? rank : 0;
   const int s0 = k_stages * k_rank / p.splits, s1 = k_stages * (k_rank + 1) / p.splits;
   const int total = p.m_tiles * p.n_tiles;
   const int per = CG > 1 ? CG : p.splits;
   const int first = blockIdx.x / per, step = gridDim.x / per;
+
+  grid_dependency_wait();
+  grid_dependents_launch();
+
   // a wait that gives up makes every later one of this CTA that is not over end soon
   const auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
     if (mbar_wait_sleeping<false>(bar, parity, p.status, site, &failed)) return true;
