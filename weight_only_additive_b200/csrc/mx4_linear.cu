@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
     // ---- results
     const int quad = warp & 3;
     const float gamma = p.gamma ? *p.gamma : 1.0f;
+    const bool out_f16 = TYPE == kF16 || (FORMAT == kMxfp4 && p.out_type == kF16);
     uint32_t n_acc = 0;
     for (int t = first; t < total; t += step, ++n_acc) {
       const uint32_t acc = accs == 2 ? n_acc & 1 : 0, acc_phase = accs == 2 ? (n_acc >> 1) & 1 : n_acc & 1;
@@ -462,11 +463,9 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
         } else if (real) {
           uint16_t* o = static_cast<uint16_t*>(p.out) + static_cast<size_t>(t0 + c) * p.features + f;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            if (c + k >= tokens) break;
+          for (int k = 0; k < 16; ++k, o += p.features) {
             const float r = fmaf(v[k], gamma, bias);
-            if (p.out_type == kF16) store_value<kF16>(o, static_cast<size_t>(k) * p.features, r);
-            else store_value<kBf16>(o, static_cast<size_t>(k) * p.features, r);
+            if (c + k < tokens) *o = out_f16 ? __half_as_ushort(__float2half_rn(r)) : __bfloat16_as_ushort(__float2bfloat16_rn(r));
           }
         }
       }
