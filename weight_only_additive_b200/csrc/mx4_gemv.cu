@@ -47,9 +47,11 @@ struct Shape {
   static constexpr int kSets = 2;
   static constexpr int kPart = kSets * kWarps * kSums * 4;
   static constexpr int kFit = (227 * 1024 - 1024 - kTableBytes - kPart - 256) / kSlot;
-  static constexpr int kSlots = kFit > 7 ? 7 : kFit;
+  // An even number, so that a slot's stages are all of one set of warps: a set that skipped a phase of
+  // a slot's barrier could take the phase before it for the one it waits for.
+  static constexpr int kSlots = kFit / 2 * 2;
   static constexpr size_t kSmem = 1024 + kTableBytes + kPart + kSlots * kSlot;
-  static_assert(kSlots >= 4, "");
+  static_assert(kSlots >= 4 && kSlots <= 8, "");
 };
 
 struct GemvParams {
@@ -151,24 +153,27 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
 
   if (warp == kWarps) {
     // ---- copies
-    if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_first();
-      Ring<S::kSlots> r;
-      bool ok = true;
-      for (int u = first; u < p.units && ok; u += step)
-        for (int s = s0; s < s1; ++s, r.next()) {
-          ok = wait(&empty[r.slot], r.phase ^ 1, kSitePipeEmpty);
-          if (!ok) break;
-          const uint32_t at = ring + r.slot * S::kSlot;
-          const int boxes = min(kStage / kBox, (p.K - s * kStage + kBox - 1) / kBox);
-          const uint32_t run = static_cast<uint32_t>(min(S::kTiles, p.tiles - s * S::kTiles)) * 512;
+    const uint64_t pol = l2_policy_evict_first();
+    const bool issuer = elect_one();
+    Ring<S::kSlots> r;
+    bool ok = true;
+    for (int u = first; u < p.units && ok; u += step)
+      for (int s = s0; s < s1; ++s, r.next()) {
+        ok = __all_sync(0xFFFFFFFFu, wait(&empty[r.slot], r.phase ^ 1, kSitePipeEmpty));
+        if (!ok) break;
+        const uint32_t at = ring + r.slot * S::kSlot;
+        const int boxes = min(kStage / kBox, (p.K - s * kStage + kBox - 1) / kBox);
+        const uint32_t run = static_cast<uint32_t>(min(S::kTiles, p.tiles - s * S::kTiles)) * 512;
+        if (issuer) {
           mbar_arrive_expect_tx(&full[r.slot], boxes * (kRows * kBox / 2) + run);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(at + b * (kRows * kBox / 2), &w_map, s * (kStage / 2) + b * (kBox / 2), u * kRows, &full[r.slot], pol);
+#pragma unroll
+          for (int b = 0; b < kStage / kBox; ++b)
+            if (b < boxes)
+              tma_load_2d(at + b * (kRows * kBox / 2), &w_map, s * (kStage / 2) + b * (kBox / 2), u * kRows, &full[r.slot], pol);
           bulk_load(at + kStageBytes, p.scales + (static_cast<size_t>(u >> 2) * p.tiles + s * S::kTiles) * 512, run,
                     &full[r.slot]);
         }
-    }
+      }
   } else if (warp == kWarps + 1) {
     // ---- the sums of the warps, in their order, while those go on with the next unit: a lane
     // a row
