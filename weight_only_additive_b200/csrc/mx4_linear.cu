@@ -52,7 +52,9 @@ struct Shape {
   // With more groups than stages in a slot, sets of groups take slots in turn.
   static constexpr int kSets = kGroups > kSlotStages ? kGroups / kSlotStages : 1;
   static constexpr int kSetGroups = kGroups / kSets;
-  static_assert(kRing % kGroups == 0 && kSlotStages % kSetGroups == 0, "");
+  // A group's stages and slots are the same ones every time round: it waits for every phase of their
+  // barriers, and none passes unseen.
+  static_assert(kRing % kGroups == 0 && kSlotStages % kSetGroups == 0 && kWSlots % kSets == 0, "");
 };
 constexpr uint32_t kATmem = 256;  // first TMEM column of the decoded stages
 
@@ -254,8 +256,9 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
   // a warp waits as one
   const auto warp_ok = [&](auto&& waits) { return __all_sync(0xFFFFFFFFu, waits()) != 0; };
 
-  if (warp == kWarpX && lane == 0) {
-    // ---- activations
+  if (warp == kWarpX) {
+    // ---- activations; the whole warp walks the stages here too, and one lane issues
+    const bool issuer = elect_one();
     const uint64_t keep = l2_policy_evict_last();
     Ring<kRing> r;
     bool ok = true;
@@ -263,18 +266,21 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
       const int row = tokens_at(t) + (CG > 1 ? rank * (p.nt / CG) : 0);
       for (int s = s0; s < s1 && ok; ++s)
         for (int j = 0; j < S::kSlotStages; ++j, r.next()) {
-          ok = wait(&done[r.slot], r.phase ^ 1, kSitePipeEmpty);
+          ok = warp_ok([&] { return wait(&done[r.slot], r.phase ^ 1, kSitePipeEmpty); });
           if (!ok) break;
           uint32_t at = smem + S::kX + r.slot * x_stage;
-          mbar_arrive_expect_tx(&ready[r.slot], x_stage);
-          for (int q = 0; q < p.parts; ++q)
+          if (issuer) {
+            mbar_arrive_expect_tx(&ready[r.slot], x_stage);
+            for (int q = 0; q < p.parts; ++q)
 #pragma unroll
-            for (int h = 0; h < S::kDepth / 64; ++h, at += x_box)
-              tma_load_2d(at, &x_map, s * kSlotDepth + j * S::kDepth + h * 64, row + q * p.batch, &ready[r.slot], keep);
+              for (int h = 0; h < S::kDepth / 64; ++h, at += x_box)
+                tma_load_2d(at, &x_map, s * kSlotDepth + j * S::kDepth + h * 64, row + q * p.batch, &ready[r.slot], keep);
+          }
         }
     }
-  } else if (warp == kWarpW && lane == 0) {
+  } else if (warp == kWarpW) {
     // ---- packed weights and scales
+    const bool issuer = elect_one();
     const uint64_t pol = p.t_tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
     const int row_tiles = ((GRAD ? p.depth : p.features) + 127) / 128;
     Ring<S::kWSlots> r;
@@ -282,7 +288,7 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
     for (int t = first; t < total && ok; t += step) {
       const int f0 = features_at(t);
       for (int s = s0; s < s1; ++s, r.next()) {
-        ok = wait(&w_empty[r.slot], r.phase ^ 1, kSitePipeCodes);
+        ok = warp_ok([&] { return wait(&w_empty[r.slot], r.phase ^ 1, kSitePipeCodes); });
         if (!ok) break;
         const uint32_t at = smem + S::kW + r.slot * kSlotBytes, sc = smem + S::kS + r.slot * kSlotScales;
         // scale tiles: along K (y), or those of the CTA's features in two row tiles (dx)
@@ -293,11 +299,13 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
         const uint32_t run = static_cast<uint32_t>(max(0, min(most, p.tiles - c0))) * 512;
         const int rows = run ? max(0, min(r_most, row_tiles - r0)) : 0;
         uint64_t* full = &w_full[r.slot];
-        mbar_arrive_expect_tx(full, kSlotBytes + rows * run);
-        if constexpr (GRAD) tma_load_2d(at, &w_map, f0 / 2, s * kSlotDepth, full, pol);
-        else tma_load_2d(at, &w_map, s * (kSlotDepth / 2), f0, full, pol);
-        for (int q = 0; q < rows; ++q)
-          bulk_load(sc + q * (kSlotScales / 2), p.scales + (static_cast<size_t>(r0 + q) * p.tiles + c0) * 512, run, full);
+        if (issuer) {
+          mbar_arrive_expect_tx(full, kSlotBytes + rows * run);
+          if constexpr (GRAD) tma_load_2d(at, &w_map, f0 / 2, s * kSlotDepth, full, pol);
+          else tma_load_2d(at, &w_map, s * (kSlotDepth / 2), f0, full, pol);
+          for (int q = 0; q < rows; ++q)
+            bulk_load(sc + q * (kSlotScales / 2), p.scales + (static_cast<size_t>(r0 + q) * p.tiles + c0) * 512, run, full);
+        }
       }
     }
   } else if (warp == kWarpMma && CG > 1 && rank > 0) {

@@ -224,8 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     return false;
   };
 
-  if (warp == 0 && lane == 0) {
-    // ---- loads
+  if (warp == 0) {
+    // ---- loads: the whole warp walks the stages, one lane issues
+    const bool issuer = elect_one();
     const uint64_t keep = l2_policy_evict_last(), pass = l2_policy_evict_first();
     const int w_row_tiles = (p.N + 127) / 128, x_row_tiles = (p.batch + 127) / 128;
     Ring<P::kStages> r;
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (int t = first; t < total && ok; t += step) {
       const int m = (t % p.m_tiles) * CG + pair_rank, n0 = (t / p.m_tiles) * NT;
       for (int s = s0; s < s1; ++s, r.next()) {
-        ok = wait(&empty[r.slot], r.phase ^ 1, kSitePipeEmpty);
+        ok = __all_sync(0xFFFFFFFFu, wait(&empty[r.slot], r.phase ^ 1, kSitePipeEmpty));
         if (!ok) break;
         uint64_t* bar = &full[r.slot];
         const uint32_t base = smem_addr(stages + r.slot * P::kStage);
@@ -242,13 +243,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const int wt = n0 / 128;
         const int w_tiles = min(P::kTilesN, w_row_tiles - wt);
         const int x_tiles = m < x_row_tiles;  // a pair's second CTA may have no tokens: it reads zeros
-        mbar_arrive_expect_tx(bar, P::kA + P::kB + run * (x_tiles + w_tiles));
-        tma_load_2d(base, &x_map, s * kRowBytes, m * kRows, bar, keep);
-        tma_load_2d(base + P::kA, &w_map, s * kRowBytes, n0 + pair_rank * (NT / CG), bar, p.m_tiles > 1 ? keep : pass);
-        const uint32_t sa = base + P::kA + P::kB, sb = sa + P::kSa;
-        if (x_tiles) bulk_load(sa, p.xs + (static_cast<size_t>(m) * p.tiles + c0) * 512, run, bar);
-        for (int j = 0; j < w_tiles; ++j)
-          bulk_load(sb + j * P::kSa, p.ws + (static_cast<size_t>(wt + j) * p.tiles + c0) * 512, run, bar);
+        if (issuer) {
+          mbar_arrive_expect_tx(bar, P::kA + P::kB + run * (x_tiles + w_tiles));
+          tma_load_2d(base, &x_map, s * kRowBytes, m * kRows, bar, keep);
+          tma_load_2d(base + P::kA, &w_map, s * kRowBytes, n0 + pair_rank * (NT / CG), bar, p.m_tiles > 1 ? keep : pass);
+          const uint32_t sa = base + P::kA + P::kB, sb = sa + P::kSa;
+          if (x_tiles) bulk_load(sa, p.xs + (static_cast<size_t>(m) * p.tiles + c0) * 512, run, bar);
+          for (int j = 0; j < w_tiles; ++j)
+            bulk_load(sb + j * P::kSa, p.ws + (static_cast<size_t>(wt + j) * p.tiles + c0) * 512, run, bar);
+        }
       }
     }
   } else if (warp == 1 && CG > 1 && rank > 0) {
