@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     bool ok = true;
     for (int t = first; t < total && ok; t += step)
       for (int s = s0; s < s1 && ok; ++s, r.next()) {
-        ok = __shfl_sync(0xFFFFFFFFu, lane == 0 ? wait(&full[r.slot], r.phase, kSitePipeFull) : false, 0);
+        ok = __all_sync(0xFFFFFFFFu, wait(&full[r.slot], r.phase, kSitePipeFull));
         if (ok && lane == 0) mbar_arrive_leader(&full[r.slot]);
       }
   } else if (warp == 1) {
@@ -327,8 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (int t = first; t < total && ok; t += step, ++acc_it) {
       const int m0 = ((t % p.m_tiles) * CG + pair_rank) * kRows, n0 = (t / p.m_tiles) * NT;
       const uint32_t acc = acc_it % P::kAccs;
-      // one lane waits for its warp
-      ok = __shfl_sync(0xFFFFFFFFu, lane == 0 ? wait(&acc_full[acc], (acc_it / P::kAccs) & 1, kSitePipeAcc) : false, 0);
+      ok = __all_sync(0xFFFFFFFFu, wait(&acc_full[acc], (acc_it / P::kAccs) & 1, kSitePipeAcc));
       if (!ok) break;
       tc_fence_after_sync();
       const int row = m0 + quad * 32 + lane;
