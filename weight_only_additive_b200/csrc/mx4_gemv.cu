@@ -21,7 +21,7 @@
 // sums come out per 16 values, and the scales multiply four fp32 sums a step instead of
 // every pair of weights.
 //
-// Measured (NVFP4 bf16): 1 token 4096 x 4096 5.4 us, 11008 x 4096 10.5, 28672 x 8192 34.8 (3.8
+// Measured (NVFP4 bf16): 1 token 4096 x 4096 5.2 us, 11008 x 4096 10.4, 28672 x 8192 33.6 (3.9
 // TB/s); 8 tokens 52 us on the last.  The loads alone take 25 us there and the arithmetic alone
 // 34: while a CTA's warps are active the shared-memory and L1 pipe is at 76 % (64 of a warp
 // step's 88 wavefronts are lookups) and 57 % of the issue slots are taken.  Decoding a quarter or
@@ -391,8 +391,8 @@ cudaError_t gemv_tokens(const Mx4Linear& c, uint32_t* status, cudaStream_t strea
 }  // namespace
 
 // Up to the eight tokens of one MMA, where this kernel is the faster (NVFP4 bf16, against the
-// decoding tensor-core kernel: 1 token 4096 x 4096 5.4 us, 9.1; 28672 x 8192 34.8, 55.1; 8 tokens
-// 6.7, 9.5 and 52, 55.3).  With two groups of tokens it was the slower of the two on large layers
+// decoding tensor-core kernel: 1 token 4096 x 4096 5.2 us, 9.1; 28672 x 8192 33.6, 53.6; 8 tokens
+// 6.6, 9.2 and 52, 53.8).  With two groups of tokens it was the slower of the two on large layers
 // (16 tokens: 8.7, 9.6 and 61.2, 55.5).
 bool mx4_gemv_takes(int batch) { return batch <= 8; }
 

@@ -29,9 +29,10 @@ constexpr int kSlotBytes = 16384, kSlotScales = 2048;
 constexpr int kTableBytes = 65536;
 constexpr int kSms = 148;
 
-// TABLE: decoding by lookup, for the tiles of few tokens, where decoding is what takes the
-// time (11008 x 4096 and 37 tokens: 24.6 us without, 18.9 with); their small stages leave room
-// for the table.
+// TABLE: decoding by lookup and by sixteen warps, for the tiles of few tokens, whose small stages
+// leave room for both (11008 x 4096 and 37 tokens: 17.4 us; 24.6 by eight warps without the table.
+// Of sixteen without it, 16 tokens and 28672 x 8192 took 59.6 us, 55.4 with; 128 and 11008 x 4096
+// 22.7, 20.9).
 template <bool GRAD, bool TABLE>
 struct Shape {
   static constexpr int kGroups = TABLE ? 4 : 2;  // of four decoding warps, which take stages in turn
@@ -567,8 +568,8 @@ struct Tiling {
 // and a tile take besides.  Measured with 4096 to 14336 features: 5.3 cycles a token of the tile,
 // but at least 840 with the table and 1400 without (dx: 1200 and 1550), which is the
 // decoding, and 250 more for x in two parts.
-// So pairs with the table take the middle (512 tokens, 4096 x 4096: 21 us, 28 without, 33 by
-// single CTAs), wide tiles without it the large batches (2048 x 4096 x 11008: 126 us, 149 with).
+// So pairs with the table take the middle (512 tokens, 4096 x 4096: 19 us, 28 without, 33 by
+// single CTAs), wide tiles without it the large batches (2048 x 4096 x 11008: 124 us, 149 with).
 Tiling plan(int features, int depth, int batch, int parts, bool grad) {
   const int slots = (depth + kSlotDepth - 1) / kSlotDepth;
   Tiling best{};

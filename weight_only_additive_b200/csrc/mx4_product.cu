@@ -11,7 +11,7 @@
 //
 // Rows of y that are not whole 16-byte units would be written value by value, a row a lane.
 // There the operands change places: a lane then has a feature, and a warp writes 32 neighbours
-// of one token (388 x 9839 x 1472: 13 us, 75 by rows).
+// of one token (388 x 9839 x 1472: 12 us, 75 by rows).
 //
 // Work: one CTA per output tile, persistent over the SMs; where there are fewer tiles
 // than SMs a cluster of CTAs shares a tile along K and adds the fp32 partial tiles through
@@ -465,7 +465,7 @@ cudaError_t product_as(const Mx4Product& p, const Mx4& a, const Mx4& b, bool swa
 // width and split on 1 to 1000 tokens of 4096 to 14336 features found nothing more than 15 %
 // faster than what this picks (64 x 14336 x 4096: 128 wide 9.4 us, 64 wide 13.5, 256 wide 12.5;
 // 64 x 4096 x 14336: 128 wide, K in four, 11.5, unsplit 20.7; 4096 x 28672 x 8192: pairs 400,
-// single 508).
+// single 508).  Loads issued by a whole warp have since taken 9.4 to 9.0 and 400 to 360.
 template <int FORMAT>
 cudaError_t product_planned(const Mx4Product& p, uint32_t* status, cudaStream_t stream) {
   const bool swapped = p.w.rows % (p.y_type == kF32 ? 4 : 8) != 0;
