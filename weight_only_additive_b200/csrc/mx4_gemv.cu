@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
         if (turn != set) continue;
         const bool any = s * kStage + kw * kStep < p.K;
         if (any) load_x(s);
-        ok = wait(&full[r.slot], r.phase, kSitePipeFull);
+        ok = __all_sync(0xFFFFFFFFu, wait(&full[r.slot], r.phase, kSitePipeFull));
         if (!ok) break;
         if (any) {
           const uint32_t at = ring + r.slot * S::kSlot;

@@ -330,13 +330,13 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
     bool ok = true;
     for (int t = first; t < total && ok; t += step, ++n_acc) {
       const uint32_t acc = accs == 2 ? n_acc & 1 : 0, acc_phase = accs == 2 ? (n_acc >> 1) & 1 : n_acc & 1;
-      ok = wait_pair(&acc_empty[acc], acc_phase ^ 1, kSitePipeAcc);
+      ok = warp_ok([&] { return wait_pair(&acc_empty[acc], acc_phase ^ 1, kSitePipeAcc); });
       tc_fence_after_sync();
       const uint32_t d = tmem + acc * acc_cols;
       uint32_t go = 0;
       for (int s = s0; s < s1 && ok; ++s)
         for (int j = 0; j < S::kSlotStages; ++j, r.next()) {
-          ok = wait_pair(&ready[r.slot], r.phase, kSitePipeFull);
+          ok = warp_ok([&] { return wait_pair(&ready[r.slot], r.phase, kSitePipeFull); });
           if (!ok) break;
           tc_fence_after_sync();
           uint64_t b = x_desc + ((r.slot * x_stage) >> 4);

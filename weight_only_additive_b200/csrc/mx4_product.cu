@@ -276,16 +276,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const int n0 = (t / p.m_tiles) * NT;
       const uint32_t shift = (n0 & 127) / 32;  // the tile's first scale column
       const uint32_t acc = acc_it % P::kAccs;
-      ok = wait_pair(&acc_empty[acc], ((acc_it / P::kAccs) & 1) ^ 1, kSitePipeAcc);
+      ok = __all_sync(0xFFFFFFFFu, wait_pair(&acc_empty[acc], ((acc_it / P::kAccs) & 1) ^ 1, kSitePipeAcc));
       tc_fence_after_sync();
       const uint32_t d = tmem + acc * NT;
       uint32_t go = 0;
       for (int s = s0; s < s1 && ok; ++s, r.next(), sc.next(), ++it) {
-        ok = wait_pair(&full[r.slot], r.phase, kSitePipeFull);
+        ok = __all_sync(0xFFFFFFFFu, wait_pair(&full[r.slot], r.phase, kSitePipeFull));
         // the scale columns' last readers: the MMAs kScaleBufs stages ago
         if (P::kScaleBufs < P::kStages && ok && it >= P::kScaleBufs) {
           const uint32_t old = it - P::kScaleBufs;
-          ok = wait(&empty[old % P::kStages], (old / P::kStages) & 1, kSitePipeEmpty);
+          ok = __all_sync(0xFFFFFFFFu, wait(&empty[old % P::kStages], (old / P::kStages) & 1, kSitePipeEmpty));
         }
         if (!ok) break;
         tc_fence_after_sync();
