@@ -25,3 +25,20 @@ def test_a_warp_waits_as_one(name):
         before = text[:m.start()]
         assert re.search(r"(__all_sync\(0xFFFFFFFFu, |warp_ok\(\[&\] \{ return )$", before), \
             (name, before.count("\n") + 1, text[m.start():m.start() + 60])
+
+
+def between(text, start, end):
+    """What follows each `start` up to the next `end`."""
+    parts = [p.split(end)[0] for p in text.split(start)[1:] if end in p]
+    assert parts, (start, end)
+    return parts
+
+
+def test_a_decoded_stage_is_overwritten_behind_a_fence():
+    """The MMAs that read a stage of tensor memory are seen to be over by a wait; the stores that
+    follow are ordered behind it by tcgen05.fence::after_thread_sync alone."""
+    text = source("mx4_linear.cu").split("tc_fence_after_sync();\n  const uint32_t tmem")[1]  # the kernel's roles
+    parts = [p for p in between(text, "wait(&done[stage]", "mbar_arrive(&ready[stage])") if "tmem_st_x32" in p]
+    assert len(parts) == 1
+    assert "tc_fence_after_sync();" in parts[0].split("tmem_st_x32")[0]
+    assert "tmem_st_wait();" in parts[0] and "tc_fence_before_sync();" in parts[0].split("tmem_st_wait();")[1]

@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
             }
             ok = warp_ok([&] { return wait(&done[stage], phase ^ 1, kSitePipeEmpty); });
             if (!ok) break;
+            tc_fence_after_sync();  // the stage's release (MMA commit) -> these tcgen05.st
 #pragma unroll
             for (int h = 0; h < S::kDepth / 64; ++h) {
               const int c = j * (S::kDepth / 64) + h;
