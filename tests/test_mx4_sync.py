@@ -42,3 +42,13 @@ def test_a_decoded_stage_is_overwritten_behind_a_fence():
     assert len(parts) == 1
     assert "tc_fence_after_sync();" in parts[0].split("tmem_st_x32")[0]
     assert "tmem_st_wait();" in parts[0] and "tc_fence_before_sync();" in parts[0].split("tmem_st_wait();")[1]
+
+
+def test_the_pair_announces_decoded_stages_between_fences():
+    """The second CTA's decoded stages are tcgen05.st results of its decoding warps, read by MMAs
+    that the first CTA issues: the warp that passes the word on is a link of that chain, with the
+    fence after its wait and the one before its arrival."""
+    parts = between(source("mx4_linear.cu"), "warp == kWarpMma && CG > 1 && rank > 0", "mbar_arrive_leader(&ready[r.slot])")
+    assert len(parts) == 1
+    order = [parts[0].find(s) for s in ("wait(&ready[r.slot]", "tc_fence_after_sync();", "tc_fence_before_sync();")]
+    assert -1 not in order and order == sorted(order)

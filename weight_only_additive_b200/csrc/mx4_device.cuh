@@ -182,7 +182,9 @@ struct Ring {
 
 // Arrive on the same barrier of the cluster's CTA 0, after this thread's shared-memory
 // accesses and those it has waited for.  The fence is restricted to shared memory: a release
-// of global memory too took about 1000 cycles a stage (2048 x 4096 x 11008: 172 -> 136 us).
+// of global memory too took about 1000 cycles a stage (2048 x 4096 x 11008: 172 -> 139 us).
+// Tensor memory is not its matter: tc_fence_before_sync() comes before the call where tcgen05
+// accesses are handed on.
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"

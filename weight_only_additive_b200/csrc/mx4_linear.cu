@@ -317,6 +317,10 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
       for (int s = s0; s < s1 && ok; ++s)
         for (int j = 0; j < S::kSlotStages && ok; ++j, r.next()) {
           ok = warp_ok([&] { return wait(&ready[r.slot], r.phase, kSitePipeFull); });
+          if constexpr (!GRAD) {  // a link between the decoding warps' tcgen05.st and the first CTA's MMAs
+            tc_fence_after_sync();
+            tc_fence_before_sync();
+          }
           if (ok && lane == 0) mbar_arrive_leader(&ready[r.slot]);
         }
   } else if (warp == kWarpMma) {
