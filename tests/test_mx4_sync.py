@@ -52,3 +52,14 @@ def test_the_pair_announces_decoded_stages_between_fences():
     assert len(parts) == 1
     order = [parts[0].find(s) for s in ("wait(&ready[r.slot]", "tc_fence_after_sync();", "tc_fence_before_sync();")]
     assert -1 not in order and order == sorted(order)
+
+
+@pytest.mark.parametrize("name", ["mx4_linear.cu", "mx4_product.cu"])
+def test_tensor_memory_is_freed_behind_a_fence(name):
+    """Other warps read it last: the barrier between is passed with both fences."""
+    text = source(name)
+    assert text.count("tmem_dealloc_cg") == 1
+    before = text.split("tmem_dealloc_cg")[0]
+    last = before.rindex("__syncthreads();")
+    assert "tc_fence_after_sync();" in before[last:]
+    assert "tc_fence_before_sync();" in before[before.rindex("}", 0, last):last]

@@ -521,6 +521,7 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
   tc_fence_before_sync();
   __syncthreads();
   if (CG > 1) cluster_sync();
+  tc_fence_after_sync();
   if (warp == kWarpMma) tmem_dealloc_cg<CG>(tmem, 512);
 }
 

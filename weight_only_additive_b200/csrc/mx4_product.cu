@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   __syncwarp();
   __syncthreads();
   if (CG > 1) cluster_sync();
+  tc_fence_after_sync();
   if (warp == 1) tmem_dealloc_cg<CG>(tmem, P::kCols);
 }
 
