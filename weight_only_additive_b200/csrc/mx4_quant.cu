@@ -99,8 +99,9 @@ __device__ __noinline__ uint32_t settle(const void* x, uint32_t codes, uint32_t 
 }
 
 // The sign of x - b c for a product within a few units in the last place of x, exact: the
-// difference to the rounded product and that product's error have few bits each.  `c_low` is
-// what c lacks.
+// difference to the rounded product and that product's error have few bits each.  The error's
+// last bit has to be one that fp32 holds: with b in multiples of 2^-9 (borders of e4m3 scales) c is
+// at least 2^-117, with whole b (borders of values) at least 2^-126.  `c_low` is what c lacks.
 __device__ __forceinline__ float beyond(float x, float b, float c, float c_low) {
   const float p = b * c;
   return (x - p) - fmaf(b, c_low, fmaf(b, c, -p));
@@ -114,7 +115,7 @@ __device__ __forceinline__ uint32_t settle_scale(float amax, float gamma, uint32
   return low + (d > 0.0f || (d == 0.0f && (low & 1)) ? 1 : 0);
 }
 
-// The same for a gamma that fp32 quotients do not hold.  The 64-bit quotient is within 2^-52 of
+// The same for a gamma whose quotients or borders fp32 does not hold.  The 64-bit quotient is within 2^-52 of
 // the exact one, which stays 2^-33 away from every tie unless it is one (its terms have 24 and
 // 27 bits), so what lies within 2^-40 of an fp32 value is that value, and anything else goes to
 // the odd fp32 neighbour: the conversion then rounds it as it would the quotient.
@@ -216,8 +217,9 @@ __global__ void __launch_bounds__(kThreads, kQuantizeCtas<TYPE>) quantize_kernel
   grid_dependents_launch();
   const float gamma = FORMAT == kNvfp4 && tensor_scale ? *tensor_scale : 1.0f;
   const bool gamma_bad = !(gamma >= 0.0f && gamma <= 3.402823466e38f);
-  // 1 / (6 gamma), or 0 where fp32 cannot hold it well
-  const float inv6 = gamma > 0x1p-120f && gamma < 0x1p100f ? 1.0f / (6.0f * gamma) : 0.0f;
+  // 1 / (6 gamma), or 0 where fp32 does not hold it well, or the errors of gamma's products with
+  // the scales' borders (beyond(): from 2^-117)
+  const float inv6 = gamma > 0x1p-100f && gamma < 0x1p100f ? 1.0f / (6.0f * gamma) : 0.0f;
   const int lane = threadIdx.x & 31;
   // 16-bit values are loaded a piece ahead; the lanes of a warp, whose pieces are neighbours,
   // go on together while any has one
