@@ -10,7 +10,8 @@ import pytest
 import torch
 
 from tests import mx4_reference as ref
-from tests.test_mx4_gpu import NV, check_quantize, dev  # noqa: F401
+from tests.test_mx4_gpu import MX, NV, check_quantize, dev, gen, once, status_ok, whole  # noqa: F401
+from weight_only_additive_b200 import mx4
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +50,31 @@ def test_quantize_with_small_tensor_scales(dev, dtype, gamma):  # noqa: F811
     if len(blocks) % 2:
         blocks.append(torch.zeros(16, dtype=dtype))
     check_quantize(torch.stack(blocks).view(-1, 32), NV, gamma, dev)
+
+
+# --------------------------------------------------------------------------
+# infinities and NaN of every pattern
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("dtype,patterns", [
+    (torch.float16, (0x7C00, 0xFC00, 0x7C01, 0xFC07, 0x7C04, 0x7E00, 0x7FFF, 0xFFFF)),
+    (torch.bfloat16, (0x7F80, 0xFF80, 0x7F81, 0xFF81, 0x7F84, 0x7FC0, 0x7FFF, 0xFFFF))])
+@pytest.mark.parametrize("batch", [1, 2, 3, 5, 8, 9, 40, 140])
+def test_special_activations_in_every_kernel(dev, fmt, dtype, patterns, batch):  # noqa: F811
+    """An infinite or NaN activation makes its token's outputs what the definition says, whatever
+    the NaN's bits, and no other token's."""
+    N, K = 70, 160
+    w, W = whole(N, K, fmt, 15, dev)
+    for i, bits in enumerate(patterns):
+        x = torch.randint(1, 4, (batch, K), generator=gen(16, i)).to(dtype)
+        at = i % batch, (37 * i + 5) % K
+        x.view(torch.int16)[at] = bits - (1 << 16 if bits >> 15 else 0)
+        assert not torch.isfinite(x[at])
+        y = mx4.matmul(x.to(dev), w).cpu()
+        want = x.double() @ W.T
+        assert torch.equal(torch.isnan(y), torch.isnan(want)), hex(bits)
+        inf = torch.isinf(want)
+        assert torch.equal(y[inf].double(), want[inf]), hex(bits)
+        fine = torch.isfinite(want)
+        assert torch.equal(y[fine], once(want[fine], dtype)), hex(bits)
+    status_ok()

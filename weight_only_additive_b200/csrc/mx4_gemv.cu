@@ -90,9 +90,12 @@ __device__ __forceinline__ void decode_pairs(const uint8_t* table, uint32_t lane
   }
 }
 
-// Two bf16 parts of a pair of fp16 values, hi + lo exactly: hi keeps 8 significant bits.
-// An infinity's second part is some finite value.
+// Two bf16 parts of a pair of fp16 values, hi + lo exactly: hi keeps 8 significant bits.  A NaN's
+// bits are made those of one that keeps some of them in hi; a second part of an infinity or a
+// NaN is some finite value.
 __device__ __forceinline__ void split_pair(uint32_t x, uint32_t& hi, uint32_t& lo) {
+  // the maximum with minus infinity: x, or 0x7FFF for a NaN
+  asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0xFC00FC00u));
   const uint32_t top = x & 0xFFF8FFF8u;
   const __half2 rest = __hmin2(__hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&top)),
                                __half2half2(__ushort_as_half(0x7BFF)));
