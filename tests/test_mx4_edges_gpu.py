@@ -16,6 +16,19 @@ from weight_only_additive_b200 import mx4
 pytestmark = pytest.mark.gpu
 
 
+def scaled(rows, K, fmt, seed, dev, low, gamma=None):
+    """Like whole(), with block scales 2^low and 2^(low + 1)."""
+    codes = torch.randint(0, 16, (rows, K), generator=gen(seed, rows, K, fmt))
+    pick = torch.randint(0, 2, (rows, K // ref.BLOCK[fmt]), generator=gen(seed, rows, K, fmt, 1))
+    if fmt == MX:
+        bytes_ = 127 + low + pick
+    else:
+        bytes_ = (1 << (low + 9)) << pick if low < -6 else 56 + 8 * (low + pick)  # 2^-9, 2^-8, 2^-7: codes 1, 2, 4
+    g = None if gamma is None else torch.tensor([gamma], dtype=torch.float32, device=dev)
+    t = mx4.Mx4Tensor.from_block_scales(ref.pack(codes).to(dev), bytes_.to(torch.uint8).to(dev), fmt, g)
+    return t, ref.values(codes, bytes_, fmt)
+
+
 # --------------------------------------------------------------------------
 # quantisation with tensor scales near the bottom of fp32
 # --------------------------------------------------------------------------
@@ -78,3 +91,44 @@ def test_special_activations_in_every_kernel(dev, fmt, dtype, patterns, batch): 
         fine = torch.isfinite(want)
         assert torch.equal(y[fine], once(want[fine], dtype)), hex(bits)
     status_ok()
+
+
+# --------------------------------------------------------------------------
+# both tensor scales of a 4-bit product
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt,low_x,low_w,gx,gw", [
+    (NV, 7, 7, 1.1e-22, 0.9e-22),      # their product is subnormal in fp32, the result is not
+    (NV, 7, 7, 3e-38, 2e-6),
+    (MX, 20, 40, 7e-30, 3e-25),        # it underflows to zero
+    (MX, 20, 40, 3e-25, 7e-30),
+    (MX, -50, -60, 3e25, 5e21),        # it overflows
+    (MX, -60, -50, -5e21, 3e25),
+    (MX, -50, -60, 7.0, 3e38)])
+@pytest.mark.parametrize("batch,N,K", [(3, 40, 64), (70, 130, 544), (70, 131, 4128), (300, 4800, 96), (300, 9601, 32)])
+def test_tensor_scales_whose_product_leaves_fp32(dev, fmt, low_x, low_w, gx, gw, batch, N, K):  # noqa: F811
+    """y = sum * gx * gw + bias: the sum is exact, two products and the sum with the bias round to
+    fp32 (half a step of 2^-24 each), then y to its type."""
+    x, X = scaled(batch, K, fmt, 31, dev, low_x, gx)
+    w, W = scaled(N, K, fmt, 32, dev, low_w, gw)
+    gx, gw = x.tensor_scale.item(), w.tensor_scale.item()
+    sums = X @ W.T
+    want = sums * gx * gw
+    assert torch.isfinite(want.float()).all() and want.abs().max() > 2.0 ** -126
+    for dtype in (torch.float32, torch.bfloat16):
+        y = mx4.matmul(x, w, out_dtype=dtype).cpu().double()
+        bound = want.abs() * (3 * 2.0 ** -24 + torch.finfo(dtype).eps / 2 * (dtype != torch.float32)) * (1 + 2.0 ** -7)
+        bound += torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+        worst = ((y - want).abs() / bound).max().item()
+        assert worst <= 1, (dtype, worst)
+        # a bias far above the product comes through
+        b = torch.full((N,), 3.0, dtype=dtype, device=dev)
+        if want.abs().max() < 2.0 ** -40:
+            assert (mx4.matmul(x, w, b, out_dtype=dtype) == 3).all()
+    status_ok()
+
+
+@pytest.mark.parametrize("gx,gw", [(0.0, 3e38), (3e38, 0.0), (0.0, 1.0)])
+def test_a_tensor_scale_of_zero(dev, gx, gw):  # noqa: F811
+    x, _ = scaled(5, 64, MX, 33, dev, 3, gx)
+    w, _ = scaled(40, 64, MX, 34, dev, 3, gw)
+    assert (mx4.matmul(x, w, out_dtype=torch.float32) == 0).all()

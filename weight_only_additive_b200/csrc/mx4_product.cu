@@ -102,6 +102,32 @@ __device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t a, uint64_t b, uin
 #undef MX4_MMA
 }
 
+// Both tensor scales as factors of a sum, v * first * second: 1 and their product, unless that
+// leaves fp32's normal range.  Then one after the other: the larger first where it is too small, so
+// that only a result that is too small itself loses bits on the way, the smaller first where it is
+// too large.  Results are written by straight code that runs once or twice, whose fetching counts:
+// the first factor has a branch of its own (64 x 14336 x 4096: 9.56 us, 9.67 multiplying every value
+// by both).
+struct TensorScales {
+  float first = 1.0f, second;
+  __device__ __forceinline__ explicit TensorScales(const ProductParams& p) {
+    const float x = p.gx ? *p.gx : 1.0f, w = p.gw ? *p.gw : 1.0f;
+    second = w * x;
+    const float a = fabsf(second);
+    if ((a < 1.17549435e-38f || a > 3.402823466e38f) && x != 0.0f && w != 0.0f) {
+      const bool x_first = (fabsf(x) > fabsf(w)) == (a < 1.0f);
+      first = x_first ? x : w;
+      second = x_first ? w : x;
+    }
+  }
+  template <int N>
+  __device__ __forceinline__ void apply_first(float (&v)[N]) const {
+    if (first != 1.0f)
+#pragma unroll
+      for (float& f : v) f *= first;
+  }
+};
+
 // bias[c .. c + 8) as fp32; `c` in whole 16-byte units
 __device__ __forceinline__ void bias8(const void* bias, int type, size_t c, float (&b)[8]) {
   if (type == kF32) {
@@ -319,8 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   } else if (warp >= 2) {
     // ---- results
     const int quad = warp & 3, half = (warp - 2) >> 2;  // TMEM lanes, half of the columns
-    float scale = p.gw ? *p.gw : 1.0f;
-    if (p.gx) scale *= *p.gx;
+    const TensorScales scales(p);
     const bool vec = p.N % (p.y_type == kF32 ? 4 : 8) == 0;
     uint32_t acc_it = 0;
     bool ok = true;
@@ -347,7 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
         const int c = half * kMine + i * 32;
-        const float* f = reinterpret_cast<const float*>(v[i]);
+        float(&f)[32] = reinterpret_cast<float(&)[32]>(v[i]);
+        if (p.splits == 1) scales.apply_first(f);
         if (p.splits > 1) {
           float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(stages) + (quad * 32 + lane) * P::kRedPitch + c);
 #pragma unroll
@@ -357,12 +383,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const float bias = bias_of(p, row);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (n0 + c + e < p.N) put_swapped(p, row, n0 + c + e, f[e], scale, bias);
+              if (n0 + c + e < p.N) put_swapped(p, row, n0 + c + e, f[e], scales.second, bias);
           }
         } else if (row < p.batch) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (n0 + c + 8 * e < p.N) put8(p, row, n0 + c + 8 * e, f + 8 * e, scale, vec);
+            if (n0 + c + 8 * e < p.N) put8(p, row, n0 + c + 8 * e, f + 8 * e, scales.second, vec);
         }
       }
     }
@@ -377,8 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int m0 = (first % p.m_tiles) * kRows, n0 = (first / p.m_tiles) * NT;
     const int rows = min(kRows, p.batch - m0), cols = min(NT, p.N - n0);
     const bool vec = p.N % (p.y_type == kF32 ? 4 : 8) == 0;
-    float scale = p.gw ? *p.gw : 1.0f;
-    if (p.gx) scale *= *p.gx;
+    const TensorScales scales(p);
     const uint32_t red = smem_addr(stages);
     for (int e = rank * kThreads + threadIdx.x; e < rows * (NT / 8); e += kThreads * p.splits) {
       const int r = p.swapped ? e % rows : e / (NT / 8), c = (p.swapped ? e / rows : e % (NT / 8)) * 8;
@@ -390,12 +415,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
         v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
       }
+      scales.apply_first(v);
       if (p.swapped) {
         const float bias = bias_of(p, m0 + r);
         for (int i = 0; i < 8; ++i)
-          if (c + i < cols) put_swapped(p, m0 + r, n0 + c + i, v[i], scale, bias);
+          if (c + i < cols) put_swapped(p, m0 + r, n0 + c + i, v[i], scales.second, bias);
       } else {
-        put8(p, m0 + r, n0 + c, v, scale, vec);
+        put8(p, m0 + r, n0 + c, v, scales.second, vec);
       }
     }
     cluster_sync();  // no CTA leaves while another reads its partial tile
