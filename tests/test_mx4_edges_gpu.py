@@ -132,3 +132,39 @@ def test_a_tensor_scale_of_zero(dev, gx, gw):  # noqa: F811
     x, _ = scaled(5, 64, MX, 33, dev, 3, gx)
     w, _ = scaled(40, 64, MX, 34, dev, 3, gw)
     assert (mx4.matmul(x, w, out_dtype=torch.float32) == 0).all()
+
+
+# --------------------------------------------------------------------------
+# activations of any magnitude
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("batch", [1, 2, 8, 9, 70])
+def test_large_activations_under_small_scales(dev, fmt, batch):  # noqa: F811
+    """Blocks whose unscaled products with x would pass the end of fp32: their scales bring them back."""
+    for N, K in ((5, 32), (130, 544), (300, 1056)):
+        w, W = scaled(N, K, fmt, 35, dev, -9)
+        x = (torch.randint(-3, 4, (batch, K), generator=gen(36, batch)).double() * 2.0 ** 120).to(torch.bfloat16)
+        y = mx4.matmul(x.to(dev), w).cpu()
+        want = x.double() @ W.T
+        assert torch.isfinite(want.float()).all()
+        assert torch.equal(y, once(want, torch.bfloat16)), (N, K)
+    # every value the largest of its type: 32 * 6 * 2^-9 of it
+    codes = torch.full((40, 32), 7)
+    bytes_ = torch.full((40, 32 // ref.BLOCK[fmt]), 118 if fmt == MX else 1)
+    w = mx4.Mx4Tensor.from_block_scales(ref.pack(codes).to(dev), bytes_.to(torch.uint8).to(dev), fmt)
+    x = torch.full((batch, 32), torch.finfo(torch.bfloat16).max, dtype=torch.bfloat16)
+    want = x.double() @ ref.values(codes, bytes_, fmt).T
+    assert torch.equal(mx4.matmul(x.to(dev), w).cpu(), once(want, torch.bfloat16))
+    status_ok()
+
+
+@pytest.mark.parametrize("batch", [1, 2, 8, 9, 70])
+def test_small_activations_under_large_scales(dev, batch):  # noqa: F811
+    """Subnormal bf16 activations that MXFP4 scales bring into the ordinary range."""
+    for N, K in ((5, 32), (130, 544)):
+        w, W = scaled(N, K, MX, 37, dev, 100)
+        x = torch.randint(-3, 4, (batch, K), generator=gen(38, batch)).double() * 2.0 ** -133
+        x = x.to(torch.bfloat16)
+        assert x.any() and (x.abs() < torch.finfo(torch.bfloat16).smallest_normal).all()
+        assert torch.equal(mx4.matmul(x.to(dev), w).cpu(), once(x.double() @ W.T, torch.bfloat16))
+    status_ok()

@@ -19,7 +19,9 @@
 // One token leaves seven of an MMA's eight columns free.  They take the blocks apart: column
 // 2 t + h holds x where lane t has half h of its 32 values and zeros elsewhere, so that the
 // sums come out per 16 values, and the scales multiply four fp32 sums a step instead of
-// every pair of weights.
+// every pair of weights.  16 products of unscaled weights with bf16 x could pass the end of fp32
+// where the scale would bring them back: there the table holds the weights times 2^-7 (16 times 6
+// is below 2^7), which fp32 sums do not lose, and the sum of all is multiplied by 2^7.
 //
 // Measured (NVFP4 bf16): 1 token 4096 x 4096 5.2 us, 11008 x 4096 10.4, 28672 x 8192 33.6 (3.9
 // TB/s); 8 tokens 52 us on the last.  The loads alone take 25 us there and the arithmetic alone
@@ -104,6 +106,10 @@ __device__ __forceinline__ void split_pair(uint32_t x, uint32_t& hi, uint32_t& l
   lo = f2_to_b2_rn(l.x, l.y);
 }
 
+// The one-token kernel's factor of the table (above).
+template <int XT>
+constexpr float kOneUp = XT == kBf16 ? 128.0f : 1.0f;
+
 // ONE: one token; else up to eight.
 template <int FORMAT, int XT, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant__ CUtensorMap w_map, const GemvParams p) {
@@ -135,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
   if (warp < kWarps) {  // the table: each warp's 16 bytes, decoded by a lane each
     uint32_t h[4];
     e2m1x8_decode<TYPE>(warp * 16 + (lane & 15), h);
+    if constexpr (ONE && XT == kBf16) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(h[0]) : "r"(0x3C003C00u));  // 2^-7
 #pragma unroll
     for (int b = 0; b < 16; ++b)
       *reinterpret_cast<uint32_t*>(table + (warp * 16 + b) * 256 + lane4) = __shfl_sync(0xFFFFFFFFu, h[0], b);
@@ -180,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
   } else if (warp == kWarps + 1) {
     // ---- the sums of the warps, in their order, while those go on with the next unit: a lane
     // a row
-    const float gamma = p.gamma ? *p.gamma : 1.0f;
+    const float gamma = p.gamma ? *p.gamma : 1.0f, up = ONE ? kOneUp<XT> : 1.0f;
     Ring<S::kSets> r;
     for (int u = first; u < p.units; u += step, r.next()) {
       if (!__all_sync(0xFFFFFFFFu, wait(&sums_full[r.slot], r.phase, kSitePipeAcc))) break;
@@ -192,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) sum += sums[k * S::kSums + token * S::kPitch];
         if (p.splits > 1) sums[token * S::kPitch] = sum;  // of this CTA's part of the reduction
-        else if (row < p.N) store_value<XT>(p.y, static_cast<size_t>(token) * p.N + row, fmaf(sum, gamma, bias));
+        else if (row < p.N) store_value<XT>(p.y, static_cast<size_t>(token) * p.N + row, fmaf(sum * up, gamma, bias));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sums_empty[r.slot]);
@@ -333,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
   settle_after_failure(failed);
   if (p.splits > 1) {  // of the one unit
     cluster_sync();
-    const float gamma = p.gamma ? *p.gamma : 1.0f;
+    const float gamma = p.gamma ? *p.gamma : 1.0f, up = ONE ? kOneUp<XT> : 1.0f;
     for (int e = rank * kThreads + threadIdx.x; e < kRows * p.batch; e += kThreads * p.splits) {
       const int row = e % kRows, token = e / kRows;
       if (first * kRows + row >= p.N) continue;
@@ -346,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
         sum += v;
       }
       const float bias = p.bias ? load_value<XT>(p.bias, first * kRows + row) : 0.0f;
-      store_value<XT>(p.y, static_cast<size_t>(token) * p.N + first * kRows + row, fmaf(sum, gamma, bias));
+      store_value<XT>(p.y, static_cast<size_t>(token) * p.N + first * kRows + row, fmaf(sum * up, gamma, bias));
     }
     cluster_sync();  // no CTA leaves while another reads its sums
   }
