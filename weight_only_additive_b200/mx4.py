@@ -41,7 +41,7 @@ def scale_tiles(rows: int, K: int, format: Format):
     return (rows + 127) // 128, -(-K // (4 * Format(format).block)), 512
 
 
-@dataclass
+@dataclass(init=False)
 class Mx4Tensor:
     """A rows x K tensor in 4 bits on a CUDA device (layout: include/mx4.h)."""
     packed: torch.Tensor                 # [rows, K/2] uint8, even k in the low four bits
@@ -49,27 +49,34 @@ class Mx4Tensor:
     format: Format
     tensor_scale: Optional[torch.Tensor] = None  # one fp32 on the device
 
-    def __post_init__(self):
+    def __init__(self, packed: torch.Tensor, scales: torch.Tensor, format: Format,
+                 tensor_scale: Optional[torch.Tensor] = None):
         # the kernels read exactly the sizes that rows, K and the format imply
-        p, s, g = self.packed, self.scales, self.tensor_scale
-        if type(self.format) is not Format:
-            self.format = Format(self.format)
-        if p.dim() != 2 or p.shape[1] == 0 or p.shape[1] % 16 or p.shape[0] == 0:
-            raise ValueError(f"packed must be [rows, K/2] with K a multiple of 32, got shape {tuple(p.shape)}")
-        dev = p.device
-        tiles = scale_tiles(p.shape[0], 2 * p.shape[1], self.format)
-        if not (p.dtype is s.dtype is torch.uint8 and s.shape == tiles and s.device == dev and p.is_contiguous()
-                and s.is_contiguous()):
-            _check_tensor(p, "packed", torch.uint8, dev)
-            _check_tensor(s, "scales", torch.uint8, dev, tiles)
-        if g is not None:
-            _check_scale(g, dev)
+        if type(format) is not Format:
+            format = Format(format)
+        if packed.dim() != 2 or packed.shape[1] == 0 or packed.shape[1] % 16 or packed.shape[0] == 0:
+            raise ValueError(f"packed must be [rows, K/2] with K a multiple of 32, got shape {tuple(packed.shape)}")
+        dev = packed.device
+        tiles = scale_tiles(packed.shape[0], 2 * packed.shape[1], format)
+        if not (packed.dtype is scales.dtype is torch.uint8 and scales.shape == tiles and scales.device == dev
+                and packed.is_contiguous() and scales.is_contiguous()):
+            _check_tensor(packed, "packed", torch.uint8, dev)
+            _check_tensor(scales, "scales", torch.uint8, dev, tiles)
+        if tensor_scale is not None:
+            _check_scale(tensor_scale, dev)
+        self.__dict__.update(packed=packed, scales=scales, format=format, tensor_scale=tensor_scale)
+
+    def __setattr__(self, name, value):
+        if name in Mx4Tensor.__dataclass_fields__:  # checked like the constructor's arguments
+            args = {f: self.__dict__[f] for f in Mx4Tensor.__dataclass_fields__}
+            value = Mx4Tensor(**{**args, name: value}).__dict__[name]
+        object.__setattr__(self, name, value)
 
     @classmethod
     def _of(cls, packed, scales, format, tensor_scale) -> "Mx4Tensor":
         """Of tensors made here, which need no checks."""
         t = object.__new__(cls)
-        t.packed, t.scales, t.format, t.tensor_scale = packed, scales, format, tensor_scale
+        t.__dict__.update(packed=packed, scales=scales, format=format, tensor_scale=tensor_scale)
         return t
 
     @property
