@@ -2,11 +2,16 @@
 with an Mx4Tensor besides calling the kernels."""
 import copy
 import dataclasses
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 from weight_only_additive_b200 import mx4
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def tensor(rows=4, K=64, fmt=1, **kw):
@@ -58,3 +63,17 @@ def test_good_assignments_copies_and_names():
     u = dataclasses.replace(t, tensor_scale=g)
     assert u.tensor_scale is g and u.packed is t.packed
     assert [f.name for f in dataclasses.fields(t)] == ["packed", "scales", "format", "tensor_scale"]
+
+
+def test_the_module_needs_no_torch_with_cuda():
+    """Of a torch built without CUDA the module can be imported, and refuses its tensors."""
+    code = ("import torch\n"
+            "del torch._C._cuda_getCurrentRawStream\n"
+            "from weight_only_additive_b200 import mx4\n"
+            "try:\n"
+            "    mx4.quantize(torch.zeros(3, 64), mx4.Format.MXFP4)\n"
+            "except ValueError as e:\n"
+            "    print(e)\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-500:]
+    assert "CUDA device" in r.stdout

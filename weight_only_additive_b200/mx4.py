@@ -146,8 +146,8 @@ def _on(dev: torch.device, stream: Optional[torch.cuda.Stream]):
 
 
 # The handle of a device's current stream (torch.cuda.current_stream builds an object, which
-# takes as long as a small kernel).
-_current = torch._C._cuda_getCurrentRawStream
+# takes as long as a small kernel).  A torch without CUDA has none, and no tensor that gets there.
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _matrix(t: torch.Tensor, name: str, cols: Optional[int], what: str, dev):
