@@ -526,10 +526,10 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
 }
 
 // Activations laid out for the kernel: rows of `pitch` values (a multiple of 8), copied, or
-// split into two bf16 parts, the second `batch` rows further on.
+// split into two bf16 parts, the second `total` values further on.
 template <bool SPLIT>
 __global__ void __launch_bounds__(256) restage_kernel(const uint16_t* __restrict__ x, uint16_t* __restrict__ out,
-                                                      long long total, int cols, int pitch, int batch) {
+                                                      long long total, int cols, int pitch) {
   grid_dependency_wait();
   grid_dependents_launch();
   for (long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; e < total;
@@ -626,7 +626,7 @@ cudaError_t launch_linear(const Call& c, const Tiling& tl, uint32_t* status, cud
     auto* out = static_cast<uint16_t*>(c.workspace);
     e = launch_overlapped(parts > 1 ? restage_kernel<true> : restage_kernel<false>,
                           static_cast<unsigned>(blocks < kSms * 64 ? blocks : kSms * 64), 256, 0, stream, 1,
-                          static_cast<const uint16_t*>(c.x), out, total, c.depth, pitch, c.batch);
+                          static_cast<const uint16_t*>(c.x), out, total, c.depth, pitch);
     if (e != cudaSuccess) return e;
     x = out;
   }
@@ -682,7 +682,7 @@ cudaError_t run(const Call& c, uint32_t* status, cudaStream_t stream) {
 }  // namespace
 
 size_t mx4_linear_workspace(int type, int format, long long K, long long batch) {
-  return batch <= 0x7FFFFFFF && mx4_gemv_takes(static_cast<int>(batch)) ? 0 : restaged_bytes(type, format, K, batch);
+  return mx4_gemv_takes(static_cast<int>(batch)) ? 0 : restaged_bytes(type, format, K, batch);
 }
 size_t mx4_grad_workspace(int type, int format, long long N, long long batch) {
   return restaged_bytes(type, format, N, batch);

@@ -160,37 +160,32 @@ __device__ __forceinline__ float bias_of(const ProductParams& p, int i) {
                             : load_value<kBf16>(p.bias, i);
 }
 
-// v[0..8) * scale + bias to y[row][c ..); `vec`: rows of y are whole 16-byte units.
-__device__ __forceinline__ void put8(const ProductParams& p, int row, int c, const float* v, float scale, bool vec) {
+// v[0..8) * scale + bias to y[row][c ..).  Rows of y are whole 16-byte units (else the operands have
+// changed places): eight values, or the last four of an fp32 row.
+__device__ __forceinline__ void put8(const ProductParams& p, int row, int c, const float* v, float scale) {
   const size_t at = static_cast<size_t>(row) * p.N + c;
-  if (vec && c + 8 <= p.N) {
-    float b[8] = {}, o[8];
-    if (p.bias) bias8(p.bias, p.y_type, c, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = fmaf(v[i], scale, b[i]);
-    if (p.y_type == kF32) {
-      float4* q = reinterpret_cast<float4*>(static_cast<float*>(p.y) + at);
-      q[0] = make_float4(o[0], o[1], o[2], o[3]);
-      q[1] = make_float4(o[4], o[5], o[6], o[7]);
-    } else {
-      uint4 q;
-      if (p.y_type == kF16)
-        q = make_uint4(f2_to_h2_rn(o[0], o[1]), f2_to_h2_rn(o[2], o[3]), f2_to_h2_rn(o[4], o[5]), f2_to_h2_rn(o[6], o[7]));
-      else
-        q = make_uint4(f2_to_b2_rn(o[0], o[1]), f2_to_b2_rn(o[2], o[3]), f2_to_b2_rn(o[4], o[5]), f2_to_b2_rn(o[6], o[7]));
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + at) = q;
-    }
+  if (c + 8 > p.N) {
+    float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (p.bias) b = *reinterpret_cast<const float4*>(static_cast<const float*>(p.bias) + c);
+    *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) =
+        make_float4(fmaf(v[0], scale, b.x), fmaf(v[1], scale, b.y), fmaf(v[2], scale, b.z), fmaf(v[3], scale, b.w));
     return;
   }
+  float b[8] = {}, o[8];
+  if (p.bias) bias8(p.bias, p.y_type, c, b);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (c + i >= p.N) break;
-    if (p.y_type == kF32)
-      store_value<kF32>(p.y, at + i, fmaf(v[i], scale, p.bias ? load_value<kF32>(p.bias, c + i) : 0.0f));
-    else if (p.y_type == kF16)
-      store_value<kF16>(p.y, at + i, fmaf(v[i], scale, p.bias ? load_value<kF16>(p.bias, c + i) : 0.0f));
+  for (int i = 0; i < 8; ++i) o[i] = fmaf(v[i], scale, b[i]);
+  if (p.y_type == kF32) {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p.y) + at);
+    q[0] = make_float4(o[0], o[1], o[2], o[3]);
+    q[1] = make_float4(o[4], o[5], o[6], o[7]);
+  } else {
+    uint4 q;
+    if (p.y_type == kF16)
+      q = make_uint4(f2_to_h2_rn(o[0], o[1]), f2_to_h2_rn(o[2], o[3]), f2_to_h2_rn(o[4], o[5]), f2_to_h2_rn(o[6], o[7]));
     else
-      store_value<kBf16>(p.y, at + i, fmaf(v[i], scale, p.bias ? load_value<kBf16>(p.bias, c + i) : 0.0f));
+      q = make_uint4(f2_to_b2_rn(o[0], o[1]), f2_to_b2_rn(o[2], o[3]), f2_to_b2_rn(o[4], o[5]), f2_to_b2_rn(o[6], o[7]));
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + at) = q;
   }
 }
 
@@ -346,7 +341,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     // ---- results
     const int quad = warp & 3, half = (warp - 2) >> 2;  // TMEM lanes, half of the columns
     const TensorScales scales(p);
-    const bool vec = p.N % (p.y_type == kF32 ? 4 : 8) == 0;
     uint32_t acc_it = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step, ++acc_it) {
@@ -388,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         } else if (row < p.batch) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (n0 + c + 8 * e < p.N) put8(p, row, n0 + c + 8 * e, f + 8 * e, scales.second, vec);
+            if (n0 + c + 8 * e < p.N) put8(p, row, n0 + c + 8 * e, f + 8 * e, scales.second);
         }
       }
     }
@@ -402,7 +396,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     cluster_sync();
     const int m0 = (first % p.m_tiles) * kRows, n0 = (first / p.m_tiles) * NT;
     const int rows = min(kRows, p.batch - m0), cols = min(NT, p.N - n0);
-    const bool vec = p.N % (p.y_type == kF32 ? 4 : 8) == 0;
     const TensorScales scales(p);
     const uint32_t red = smem_addr(stages);
     for (int e = rank * kThreads + threadIdx.x; e < rows * (NT / 8); e += kThreads * p.splits) {
@@ -421,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         for (int i = 0; i < 8; ++i)
           if (c + i < cols) put_swapped(p, m0 + r, n0 + c + i, v[i], scales.second, bias);
       } else {
-        put8(p, m0 + r, n0 + c, v, scales.second, vec);
+        put8(p, m0 + r, n0 + c, v, scales.second);
       }
     }
     cluster_sync();  // no CTA leaves while another reads its partial tile

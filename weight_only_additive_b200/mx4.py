@@ -117,11 +117,6 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _check(status: int, what: str):
-    if status:
-        raise native.AqlmError(status, what)
-
-
 def _check_scale(g: torch.Tensor, dev):
     _check_tensor(g, "tensor_scale", torch.float32, dev)
     if g.numel() != 1:
@@ -187,8 +182,8 @@ def quantize(x: torch.Tensor, format: Format, tensor_scale: Optional[torch.Tenso
         up, across, _ = scale_tiles(rows, K, fmt)
         out = Mx4Tensor._of(torch.empty(rows, K // 2, dtype=torch.uint8, device=dev),
                             torch.empty(up, across, 512, dtype=torch.uint8, device=dev), fmt, tensor_scale)
-    _check(native.lib().mx4_quantize(x.data_ptr(), xt, out.packed.data_ptr(), out.scales.data_ptr(),
-                                     _ptr(tensor_scale), rows, K, fmt, _current(dev.index)), "mx4_quantize")
+    native.mx4_quantize(x.data_ptr(), xt, out.packed.data_ptr(), out.scales.data_ptr(), _ptr(tensor_scale), rows, K,
+                        fmt, _current(dev.index))
     return out
 
 
@@ -206,8 +201,8 @@ def dequantize(t: Mx4Tensor, dtype: torch.dtype = torch.float16, out: Optional[t
             return dequantize(t, dtype, out)
     if out is None:
         out = torch.empty(rows, 2 * half, dtype=dtype, device=dev)
-    _check(native.lib().mx4_dequantize(packed.data_ptr(), t.scales.data_ptr(), _ptr(t.tensor_scale), out.data_ptr(),
-                                       code, rows, 2 * half, t.format, _current(dev.index)), "mx4_dequantize")
+    native.mx4_dequantize(packed.data_ptr(), t.scales.data_ptr(), _ptr(t.tensor_scale), out.data_ptr(), code, rows,
+                          2 * half, t.format, _current(dev.index))
     return out
 
 
@@ -255,18 +250,16 @@ def matmul(x: Union[torch.Tensor, Mx4Tensor], w: Mx4Tensor, bias: Optional[torch
     if out is None:
         out = torch.empty(batch, N, dtype=out_dtype, device=dev)
     if four:
-        _check(native.lib().mx4_matmul_mx4(x.packed.data_ptr(), x.scales.data_ptr(), _ptr(x.tensor_scale),
-                                           packed.data_ptr(), w.scales.data_ptr(), _ptr(w.tensor_scale), _ptr(bias),
-                                           out.data_ptr(), code, N, K, batch, w.format, _current(dev.index)),
-               "mx4_matmul_mx4")
+        native.mx4_matmul_mx4(x.packed.data_ptr(), x.scales.data_ptr(), _ptr(x.tensor_scale), packed.data_ptr(),
+                              w.scales.data_ptr(), _ptr(w.tensor_scale), _ptr(bias), out.data_ptr(), code, N, K, batch,
+                              w.format, _current(dev.index))
     else:
         ws, need = None, 0
         if code == 0 and not w.format:  # fp16 x with MXFP4 weights alone can need one
             need = native.mx4_matmul_workspace_size(code, N, K, batch, w.format)
             ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-        _check(native.lib().mx4_matmul(x.data_ptr(), code, packed.data_ptr(), w.scales.data_ptr(),
-                                       _ptr(w.tensor_scale), _ptr(bias), out.data_ptr(), N, K, batch, w.format,
-                                       _ptr(ws), need, _current(dev.index)), "mx4_matmul")
+        native.mx4_matmul(x.data_ptr(), code, packed.data_ptr(), w.scales.data_ptr(), _ptr(w.tensor_scale), _ptr(bias),
+                          out.data_ptr(), N, K, batch, w.format, _ptr(ws), need, _current(dev.index))
     return out
 
 
@@ -291,7 +284,6 @@ def input_grad(dy: torch.Tensor, w: Mx4Tensor, out: Optional[torch.Tensor] = Non
         out = torch.empty(batch, 2 * half, dtype=dy.dtype, device=dev)
     need = native.mx4_input_grad_workspace_size(code, N, 2 * half, batch, w.format)
     ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-    _check(native.lib().mx4_input_grad(dy.data_ptr(), code, packed.data_ptr(), w.scales.data_ptr(),
-                                       _ptr(w.tensor_scale), out.data_ptr(), N, 2 * half, batch, w.format, _ptr(ws),
-                                       need, _current(dev.index)), "mx4_input_grad")
+    native.mx4_input_grad(dy.data_ptr(), code, packed.data_ptr(), w.scales.data_ptr(), _ptr(w.tensor_scale),
+                          out.data_ptr(), N, 2 * half, batch, w.format, _ptr(ws), need, _current(dev.index))
     return out
