@@ -14,17 +14,35 @@ def source(name):
     return re.sub(r"//[^\n]*", "", text)
 
 
+def mma_role(text):
+    """The role that issues MMAs, where there is one: only its elected lane does anything."""
+    start = re.search(r"\} else if \(warp == (kWarpMma|1)\) \{", text)
+    return text[start.start():text.index("umma_commit_cg<CG>(&acc_full[acc])")] if start else ""
+
+
 @pytest.mark.parametrize("name", ["mx4_gemv.cu", "mx4_linear.cu", "mx4_product.cu"])
 def test_a_warp_waits_as_one(name):
     """Every bounded wait of a role is agreed on by the warp: whole-warp instructions follow, and
     lanes that gave up would leave the others in them for good."""
     text = source(name)
+    text = text.replace(mma_role(text), "")
     waits = list(re.finditer(r"\bwait(?:_pair)?\(&", text))
     assert waits
     for m in waits:
         before = text[:m.start()]
         assert re.search(r"(__all_sync\(0xFFFFFFFFu, |warp_ok\(\[&\] \{ return )$", before), \
             (name, before.count("\n") + 1, text[m.start():m.start() + 60])
+
+
+@pytest.mark.parametrize("name", ["mx4_linear.cu", "mx4_product.cu"])
+def test_the_warp_that_issues_agrees_once_a_tile(name):
+    """There the lanes wait by themselves: no whole-warp instruction stands between the waits of a
+    tile, and the warp agrees before the tile's commit."""
+    role = mma_role(source(name))
+    assert len(re.findall(r"\bwait(?:_pair)?\(&", role)) >= 2
+    tile, agreed = role.split("for (int t = first;")[1].split("ok = __all_sync(0xFFFFFFFFu, ok);")
+    assert not re.search(r"_sync\(|\.aligned|shfl|tmem_ld|tmem_st", tile.replace("tc_fence_after_sync();", ""))
+    assert agreed.strip() == "if (ok && issuer)"
 
 
 def between(text, start, end):

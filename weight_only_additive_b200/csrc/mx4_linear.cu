@@ -325,7 +325,9 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
         }
   } else if (warp == kWarpMma) {
     // ---- MMAs: the whole warp walks the stages, so that descriptors stay in uniform
-    // registers; one lane issues
+    // registers; one lane issues.  The lanes wait by themselves, since no whole-warp instruction
+    // follows within a tile, and agree at its end (agreeing at every stage: 1 to 2 % of the time
+    // of few tokens)
     const uint32_t idesc = linear_idesc<TYPE, GRAD>(kF * CG, p.nt);
     const bool issuer = elect_one();
     const uint64_t x_desc = umma_desc_sw128_kmajor(smem + S::kX), a_desc = mn_desc(smem);
@@ -334,13 +336,13 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
     bool ok = true;
     for (int t = first; t < total && ok; t += step, ++n_acc) {
       const uint32_t acc = accs == 2 ? n_acc & 1 : 0, acc_phase = accs == 2 ? (n_acc >> 1) & 1 : n_acc & 1;
-      ok = warp_ok([&] { return wait_pair(&acc_empty[acc], acc_phase ^ 1, kSitePipeAcc); });
+      ok = wait_pair(&acc_empty[acc], acc_phase ^ 1, kSitePipeAcc);
       tc_fence_after_sync();
       const uint32_t d = tmem + acc * acc_cols;
       uint32_t go = 0;
       for (int s = s0; s < s1 && ok; ++s)
         for (int j = 0; j < S::kSlotStages; ++j, r.next()) {
-          ok = warp_ok([&] { return wait_pair(&ready[r.slot], r.phase, kSitePipeFull); });
+          ok = wait_pair(&ready[r.slot], r.phase, kSitePipeFull);
           if (!ok) break;
           tc_fence_after_sync();
           uint64_t b = x_desc + ((r.slot * x_stage) >> 4);
@@ -363,6 +365,7 @@ __global__ void __launch_bounds__(Shape<GRAD, TABLE>::kThreads, 1) linear_kernel
           }
           go = 1;
         }
+      ok = __all_sync(0xFFFFFFFFu, ok);
       if (ok && issuer) umma_commit_cg<CG>(&acc_full[acc]);
     }
   } else if (warp >= kWarpDecode && warp < kWarpOut) {

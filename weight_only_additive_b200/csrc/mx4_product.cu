@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       }
   } else if (warp == 1) {
     // ---- scale copies and MMAs: the whole warp walks the stages, so that descriptors stay
-    // in uniform registers; one lane issues
+    // in uniform registers; one lane issues.  The lanes wait by themselves, since no whole-warp
+    // instruction follows within a tile, and agree at its end
     const bool issuer = elect_one();
     const uint64_t a_desc = umma_desc_sw128_kmajor(smem_addr(stages)), s_desc = scales_desc(smem_addr(stages) + P::kA + P::kB);
     Ring<P::kStages> r;
@@ -297,16 +298,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const int n0 = (t / p.m_tiles) * NT;
       const uint32_t shift = (n0 & 127) / 32;  // the tile's first scale column
       const uint32_t acc = acc_it % P::kAccs;
-      ok = __all_sync(0xFFFFFFFFu, wait_pair(&acc_empty[acc], ((acc_it / P::kAccs) & 1) ^ 1, kSitePipeAcc));
+      ok = wait_pair(&acc_empty[acc], ((acc_it / P::kAccs) & 1) ^ 1, kSitePipeAcc);
       tc_fence_after_sync();
       const uint32_t d = tmem + acc * NT;
       uint32_t go = 0;
       for (int s = s0; s < s1 && ok; ++s, r.next(), sc.next(), ++it) {
-        ok = __all_sync(0xFFFFFFFFu, wait_pair(&full[r.slot], r.phase, kSitePipeFull));
+        ok = wait_pair(&full[r.slot], r.phase, kSitePipeFull);
         // the scale columns' last readers: the MMAs kScaleBufs stages ago
         if (P::kScaleBufs < P::kStages && ok && it >= P::kScaleBufs) {
           const uint32_t old = it - P::kScaleBufs;
-          ok = __all_sync(0xFFFFFFFFu, wait(&empty[old % P::kStages], (old / P::kStages) & 1, kSitePipeEmpty));
+          ok = wait(&empty[old % P::kStages], (old / P::kStages) & 1, kSitePipeEmpty);
         }
         if (!ok) break;
         tc_fence_after_sync();
@@ -335,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         go = 1;
       }
+      ok = __all_sync(0xFFFFFFFFu, ok);
       if (ok && issuer) umma_commit_cg<CG>(&acc_full[acc]);
     }
   } else if (warp >= 2) {
