@@ -10,8 +10,8 @@
  *           blocks, 512 bytes a tile, tiles row-major [ceil(rows/128)][ceil(K/block/4)]:
  *           block c of row r is byte (r % 32) * 16 + (r % 128) / 32 * 4 + c % 4 of tile
  *           (r / 128, c / 4) -- the order in which the tensor cores take scales.
- *           The blocks after K/block in the last tile of a row hold 0; rows after the
- *           last one may hold anything.
+ *           The blocks after K/block in the last tile of a row hold 0 (they are read, and
+ *           not checked); rows after the last one may hold anything.
  *     MX4_MXFP4  block 32, e8m0: code c is 2^(c - 127), 255 is NaN
  *     MX4_NVFP4  block 16, e4m3 (no sign): 0x7F is NaN
  *   tensor_scale  one fp32 on the device, or NULL for 1

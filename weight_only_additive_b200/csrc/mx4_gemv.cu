@@ -1,5 +1,6 @@
-// y = x . W^T + bias with 16-bit x and microscaled 4-bit W, for up to eight tokens.  The weights are decoded in registers and multiplied by mma.sync (16 rows x
-// 8 tokens x 16 values), which keeps the arithmetic per weight well below fp32 FMAs.
+// y = x . W^T + bias with 16-bit x and microscaled 4-bit W, for up to eight tokens.  The weights
+// are decoded in registers and multiplied by mma.sync (16 rows x 8 tokens x 16 values), which
+// keeps the arithmetic per weight well below fp32 FMAs.
 //
 // Persistent CTAs, one an SM, walk units of 32 weight rows.  A stage is 1024 values of them:
 // four 128-byte-swizzled TMA boxes and the scale tiles, in a ring that runs across units, so
@@ -12,9 +13,9 @@
 //
 // Decoding is a table lookup: a byte of two codes gives their pair.  The table has a copy
 // for every lane, each in its own bank, 256 bytes a row, so that one byte permute makes
-// the address and no lookup conflicts.  Eight weights cost a lane four of each.  The decoded weight is exact: e2m1 times 2^e or e4m3
-// fits bf16, e2m1 times e4m3 fits fp16.  fp16 x with MXFP4 weights is split into two bf16
-// parts.
+// the address and no lookup conflicts.  Eight weights cost a lane four of each.  The decoded
+// weight is exact: e2m1 times 2^e or e4m3 fits bf16, e2m1 times e4m3 fits fp16.  fp16 x with
+// MXFP4 weights is split into two bf16 parts.
 //
 // One token leaves seven of an MMA's eight columns free.  They take the blocks apart: column
 // 2 t + h holds x where lane t has half h of its 32 values and zeros elsewhere, so that the
@@ -24,10 +25,11 @@
 // is below 2^7), which fp32 sums do not lose, and the sum of all is multiplied by 2^7.
 //
 // Measured (NVFP4 bf16): 1 token 4096 x 4096 5.2 us, 11008 x 4096 10.4, 28672 x 8192 33.6 (3.9
-// TB/s); 8 tokens 52 us on the last.  The loads alone take 25 us there and the arithmetic alone
-// 34: while a CTA's warps are active the shared-memory and L1 pipe is at 76 % (64 of a warp
-// step's 88 wavefronts are lookups) and 57 % of the issue slots are taken.  Decoding a quarter or
-// half of the words by logic instead was slower (37 and 43 us), as were three sets of warps.
+// TB/s); 8 tokens 52 us on the last.  While a CTA's warps are active the shared-memory and L1 pipe
+// is at 78 % (64 of a warp step's 88 wavefronts are lookups) and 58 % of the issue slots are taken.
+// When the kernel took 36.5 us for one token there, its loads alone took 25 and its arithmetic
+// alone 34.6; decoding a quarter or half of the words by logic instead was slower (37 and 43 us),
+// as were three sets of warps (37.7).
 #include "mx4_device.cuh"
 
 namespace aqlm {

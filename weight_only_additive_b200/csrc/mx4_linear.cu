@@ -3,12 +3,13 @@
 // tensor-core path with the weights decoded on chip.
 //
 // The MMA's rows (TMEM lanes) are 128 output features a CTA, its columns a tile of up to
-// 256 tokens.  Eight warps decode the weights of a stage (64 values of the reduction)
-// exactly: e2m1 times an e4m3 scale fits fp16 and bf16, e2m1 times a power of two fits
-// bf16.  For y a lane's 64 values go to tensor memory, which takes the decoded operand off
-// the shared-memory ports; for dx, where the reduction runs over weight rows, they go to
-// shared memory with the features contiguous (MN-major).  Packed weights and scales arrive
-// by TMA in a ring of 256-deep slots, activations in one of 64-deep stages.
+// 256 tokens.  Eight warps, or sixteen with a lookup table where a tile has few tokens, decode
+// the weights of a stage (128 values of the reduction for y, 64 for dx) exactly: e2m1 times an
+// e4m3 scale fits fp16 and bf16, e2m1 times a power of two fits bf16.  For y a lane's values go
+// to tensor memory, which takes the decoded operand off the shared-memory ports; for dx, where
+// the reduction runs over weight rows, they go to shared memory with the features contiguous
+// (MN-major).  Packed weights and scales arrive by TMA in a ring of 256-deep slots,
+// activations in one of stages.
 //
 // With many tokens two CTAs form a pair (cta_group::2): 256 features x 256 tokens, each
 // decoding its own 128 features and loading half of the tokens, which halves the L2 traffic
@@ -38,7 +39,7 @@ struct Shape {
   static constexpr int kGroups = TABLE ? 4 : 2;  // of four decoding warps, which take stages in turn
   static constexpr int kWarpX = 0, kWarpMma = 1, kWarpDecode = 2, kWarpOut = 2 + 4 * kGroups, kWarpW = kWarpOut + 4;
   static constexpr int kThreads = (kWarpW + 1) * 32;
-  // Reduction depth of a stage.  Every stage costs the MMA thread a wait and a commit, so
+  // Reduction depth of a stage.  Every stage costs the warp that issues a wait and a commit, so
   // deep ones; dx's decoded stages lie in shared memory, which has room for 64.
   static constexpr int kDepth = GRAD ? 64 : 128;
   static constexpr int kSlotStages = kSlotDepth / kDepth;

@@ -7,7 +7,8 @@
 // bounds a single CTA's tile.  A stage is 256 values of K: 128-byte packed
 // rows of both operands by TMA (128-byte swizzle) and their scales as whole 512-byte
 // tiles, which tcgen05.cp spreads over the four TMEM lane quadrants as the MMA wants
-// them.  One thread loads, one issues copies and MMAs, eight warps write results.
+// them.  A lane of one warp issues the loads, a lane of another the scale copies and MMAs; eight
+// warps write results.
 //
 // Rows of y that are not whole 16-byte units would be written value by value, a row a lane.
 // There the operands change places: a lane then has a feature, and a warp writes 32 neighbours
@@ -106,8 +107,8 @@ __device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t a, uint64_t b, uin
 // leaves fp32's normal range.  Then one after the other: the larger first where it is too small, so
 // that only a result that is too small itself loses bits on the way, the smaller first where it is
 // too large.  Results are written by straight code that runs once or twice, whose fetching counts:
-// the first factor has a branch of its own (64 x 14336 x 4096: 9.56 us, 9.67 multiplying every value
-// by both).
+// the first factor has a branch of its own (multiplying every value by both took 0.1 us more of 9.5,
+// 64 x 14336 x 4096).
 struct TensorScales {
   float first = 1.0f, second;
   __device__ __forceinline__ explicit TensorScales(const ProductParams& p) {
@@ -486,8 +487,13 @@ cudaError_t product_as(const Mx4Product& p, const Mx4& a, const Mx4& b, bool swa
 // a rate of 128 x 256 x 64 in 128 cycles) or its loads, plus filling and draining.  Forcing each
 // width and split on 1 to 1000 tokens of 4096 to 14336 features found nothing more than 15 %
 // faster than what this picks (64 x 14336 x 4096: 128 wide 9.4 us, 64 wide 13.5, 256 wide 12.5;
-// 64 x 4096 x 14336: 128 wide, K in four, 11.5, unsplit 20.7; 4096 x 28672 x 8192: pairs 400,
-// single 508).  Loads issued by a whole warp have since taken 9.4 to 9.0 and 400 to 360.
+// 64 x 4096 x 14336: 128 wide, K in four, 11.5, unsplit 20.7); the kernel now takes 8.8 for the
+// first.  Reading the weights from HBM, which bounds fewer tokens, is not in the costs.
+//
+// Pairs are outside the costs too: they are taken wherever they make at least 37 tiles (4096 x
+// 28672 x 8192: 400 us, single tiles 508; 354 now).  Where their tiles fill the 74 places badly
+// (5120 features: 40 tiles at 512 tokens, 14.7 us; 80 at 1024, 22.7) single ones have not been
+// compared.
 template <int FORMAT>
 cudaError_t product_planned(const Mx4Product& p, uint32_t* status, cudaStream_t stream) {
   const bool swapped = p.w.rows % (p.y_type == kF32 ? 4 : 8) != 0;

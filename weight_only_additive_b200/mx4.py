@@ -43,7 +43,11 @@ def scale_tiles(rows: int, K: int, format: Format):
 
 @dataclass(init=False)
 class Mx4Tensor:
-    """A rows x K tensor in 4 bits on a CUDA device (layout: include/mx4.h)."""
+    """A rows x K tensor in 4 bits on a CUDA device (layout: include/mx4.h).
+
+    Types and sizes are checked, the scales' bytes are not read: those behind a row's last
+    block must be 0, as quantize() and from_block_scales() leave them (a NaN code there
+    would reach the row's results)."""
     packed: torch.Tensor                 # [rows, K/2] uint8, even k in the low four bits
     scales: torch.Tensor                 # [row tiles, tiles along K, 512] uint8
     format: Format
@@ -213,7 +217,8 @@ def matmul(x: Union[torch.Tensor, Mx4Tensor], w: Mx4Tensor, bias: Optional[torch
 
     x: a [batch, K] fp16 or bf16 tensor (weights taken exactly; y in x's type), or an
     Mx4Tensor of w's format, whose product runs on the block-scaled tensor-core path (y
-    in out_dtype: fp16, bf16 or fp32; out's or bias's type if None, else fp16).
+    in out_dtype: fp16, bf16 or fp32; out's or bias's type if None, else fp16, which ends at
+    65504: a 4-bit tensor does not know the type that it was quantised from, so name it).
     bias: [N] in y's type."""
     four = isinstance(x, Mx4Tensor)
     packed = w.packed
